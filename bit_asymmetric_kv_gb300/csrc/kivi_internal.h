@@ -177,4 +177,56 @@ struct Fp16Args {
 void fp16_plan(int B, int Hkv, int64_t n, int num_sms, int *splits, int64_t *tiles_per_split);
 cudaError_t launch_fp16(const Fp16Args &a, cudaStream_t st);
 
+// Prompts packed into one token axis: element (token, head, channel) of a tensor is
+// p[token * ts + head * hs + channel], strides in elements (multiples of 8).
+struct PackedRows {
+  uint16_t *p;
+  int64_t ts, hs;
+};
+
+struct PackedAttentionArgs {
+  PackedRows q, k, v, out;
+  const int32_t *cu;  // [n_seqs + 1] row bounds on the device
+  int n_seqs;         // <= kPackedMaxSeqs
+  int T;              // rows of the token axis
+  int Hq, Hkv;
+  float softmax_scale;
+};
+cudaError_t launch_packed_attention(const PackedAttentionArgs &a, cudaStream_t st);
+
+// The packed prompts quantized into the pages of their sequences.
+struct PackedQuantArgs {
+  PackedRows k, v;
+  const int32_t *cu;  // [B + 1]
+  const int32_t *bt;  // [B][max_pages]
+  int32_t *seq_lens;  // [B]
+  uint16_t *k_res;    // [B][Hkv][G][128]
+  uint16_t *v_res;    // the same with a value residual, else null
+  uint32_t *k_codes, *k_meta, *v_codes, *v_meta;
+  int64_t num_pages;
+  int B, Hkv, G, bits, shift, max_pages, T;
+};
+cudaError_t launch_packed_quantize(const PackedQuantArgs &a, cudaStream_t st);
+
+// Pages of a paged cache handed out, shared, copied, given back and moved
+// (kivi_pages.cu).  A page is free when its reference count is not positive; a table
+// entry outside [0, num_pages) holds no page.
+struct PoolArgs {
+  uint32_t *k_codes, *k_meta, *v_codes, *v_meta;
+  uint16_t *k_res, *v_res;
+  int32_t *bt;         // [B][max_pages]
+  int32_t *seq_lens;   // [B]
+  int32_t *refs;       // [num_pages]
+  int32_t *info;       // [4]
+  const int32_t *arg;  // reserve: extra tokens [B]; reorder: parent [B]
+  int32_t *new_ids;    // compact: [num_pages]
+  void *ws;
+  int num_pages;
+  int B, Hkv, G, bits, shift, max_pages;
+};
+size_t pool_workspace_bytes(int B, int Hkv, int G, int max_pages, int64_t num_pages, bool value_residual);
+cudaError_t launch_pool_reserve(const PoolArgs &a, cudaStream_t st);
+cudaError_t launch_pool_reorder(const PoolArgs &a, cudaStream_t st);
+cudaError_t launch_pool_compact(const PoolArgs &a, cudaStream_t st);
+
 }  // namespace kivi
