@@ -1,6 +1,7 @@
 // kivi_api.cu -- the C ABI (include/kivi.h): argument checks, then kernel launches.
 // Nothing here allocates device memory, synchronises with the host or keeps state.
 #include <cuda_runtime.h>
+#include <float.h>
 #include <stdint.h>
 
 #include "../../include/kivi.h"
@@ -177,6 +178,76 @@ kivi::DecodeArgs paged_decode_args(const kivi_paged_dims *d, const kivi_paged_ca
   a.page_shift = page_shift_of(d->page_tokens);
   a.max_pages = d->max_pages_per_seq;
   a.cap_tokens = paged_cap(d);
+  return a;
+}
+
+// ---- packed prompts and pages
+constexpr int64_t kMaxStride = 1ll << 38;
+
+int check_rows(const kivi_rows *r) {
+  if (!r || !r->data) return KIVI_ERR_ARG;
+  if (r->token_stride < 128 || r->head_stride < 128) return KIVI_ERR_ARG;
+  if (r->token_stride > kMaxStride || r->head_stride > kMaxStride) return KIVI_ERR_UNSUPPORTED;
+  if (!aligned16(r->data) || r->token_stride % 8 != 0 || r->head_stride % 8 != 0) return KIVI_ERR_ALIGN;
+  return KIVI_OK;
+}
+
+// No two elements of an output at one address: one axis strides over the whole other one.
+bool rows_apart(const kivi_rows *r, int64_t tokens, int64_t heads) {
+  if (tokens <= 1 || heads <= 1) return true;
+  const auto over = [](int64_t outer, int64_t inner, int64_t n) { return (outer - 128) / inner >= n - 1; };
+  return over(r->token_stride, r->head_stride, heads) || over(r->head_stride, r->token_stride, tokens);
+}
+
+kivi::PackedRows packed_rows(const kivi_rows *r) {
+  return kivi::PackedRows{r->data, r->token_stride, r->head_stride};
+}
+
+int check_packed(int32_t n_seqs, const int32_t *cu, int64_t n_tokens) {
+  if (n_seqs <= 0 || n_tokens < 0 || !cu) return KIVI_ERR_ARG;
+  if (n_seqs > kivi::kPagedMaxBatch || n_tokens > INT32_MAX) return KIVI_ERR_UNSUPPORTED;
+  if (!aligned4(cu)) return KIVI_ERR_ALIGN;
+  return KIVI_OK;
+}
+
+size_t pool_bytes(const kivi_paged_dims *d) {
+  return kivi::pool_workspace_bytes(d->B, d->Hkv, d->G, d->max_pages_per_seq, d->num_pages, d->value_residual != 0);
+}
+
+// The checks that the three page calls share; `list` is the call's own int32 array.
+int check_pool(const kivi_paged_dims *d, const kivi_paged_cache *c, const kivi_page_pool *p, const int32_t *list,
+               const void *ws, size_t ws_bytes) {
+  int s = check_paged_dims(d);
+  if (s != KIVI_OK) return s;
+  if ((s = check_paged_cache(d, c)) != KIVI_OK) return s;
+  if (d->num_pages > (1 << 30)) return KIVI_ERR_UNSUPPORTED;
+  if (!p || !p->ref_counts || !p->info || !list || p->block_table != c->block_table) return KIVI_ERR_ARG;
+  if (!aligned16(p->ref_counts) || !aligned4(p->info) || !aligned4(list)) return KIVI_ERR_ALIGN;
+  if (!ws || ws_bytes < pool_bytes(d)) return KIVI_ERR_WORKSPACE;
+  if (!aligned16(ws)) return KIVI_ERR_ALIGN;
+  return KIVI_OK;
+}
+
+kivi::PoolArgs pool_args(const kivi_paged_dims *d, const kivi_paged_cache *c, const kivi_page_pool *p, void *ws) {
+  kivi::PoolArgs a = {};
+  a.k_codes = c->k_codes;
+  a.k_meta = c->k_meta;
+  a.v_codes = c->v_codes;
+  a.v_meta = c->v_meta;
+  a.k_res = c->k_res;
+  a.v_res = paged_vres(d, c);
+  a.bt = p->block_table;
+  a.seq_lens = c->seq_lens;
+  a.refs = p->ref_counts;
+  a.info = p->info;
+  a.ws = ws;
+  a.num_pages = (int)d->num_pages;
+  a.B = d->B;
+  a.Hkv = d->Hkv;
+  a.G = d->G;
+  a.bits = d->bits;
+  a.shift = page_shift_of(d->page_tokens);
+  a.max_pages = d->max_pages_per_seq;
   return a;
 }
 
@@ -566,6 +637,100 @@ int kivi_paged_decode_step(const kivi_paged_dims *d, const kivi_paged_cache *c, 
   a.len_offset = 1;
   a.advance_lens = c->seq_lens;
   return cuda_status(kivi::launch_paged_decode(a, st));
+}
+
+// --------------------------------------------------------------------- packed prompts
+int kivi_prefill_attention_packed(int32_t Hq, int32_t Hkv, int32_t D, int32_t n_seqs, const int32_t *cu_seqlens,
+                                  int64_t n_tokens, const kivi_rows *q, const kivi_rows *k, const kivi_rows *v,
+                                  float softmax_scale, const kivi_rows *out, cudaStream_t st) {
+  if (Hq <= 0 || Hkv <= 0) return KIVI_ERR_ARG;
+  if (D != 128 || Hq % Hkv != 0) return KIVI_ERR_UNSUPPORTED;
+  int s = check_packed(n_seqs, cu_seqlens, n_tokens);
+  if (s != KIVI_OK) return s;
+  for (const kivi_rows *r : {q, k, v, out})
+    if ((s = check_rows(r)) != KIVI_OK) return s;
+  if (!rows_apart(out, n_tokens, Hq)) return KIVI_ERR_ARG;
+  if (!(softmax_scale > 0.f) || !(softmax_scale <= FLT_MAX)) return KIVI_ERR_ARG;
+  kivi::PackedAttentionArgs a = {};
+  a.q = packed_rows(q);
+  a.k = packed_rows(k);
+  a.v = packed_rows(v);
+  a.out = packed_rows(out);
+  a.cu = cu_seqlens;
+  a.n_seqs = n_seqs;
+  a.T = (int)n_tokens;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.softmax_scale = softmax_scale;
+  if (!kivi::packed_attention_fits(a)) return KIVI_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return KIVI_OK;
+  return cuda_status(kivi::launch_packed_attention(a, st));
+}
+
+int kivi_paged_prefill_packed(const kivi_paged_dims *d, const kivi_paged_cache *c, const int32_t *cu_seqlens,
+                              int64_t n_tokens, const kivi_rows *k, const kivi_rows *v, cudaStream_t st) {
+  int s = check_paged_dims(d);
+  if (s != KIVI_OK) return s;
+  if ((s = check_paged_cache(d, c)) != KIVI_OK) return s;
+  if ((s = check_packed(d->B, cu_seqlens, n_tokens)) != KIVI_OK) return s;
+  for (const kivi_rows *r : {k, v})
+    if ((s = check_rows(r)) != KIVI_OK) return s;
+  if (d->Hkv > 65535) return KIVI_ERR_UNSUPPORTED;  // grid.y of the launch
+  if (n_tokens == 0) return KIVI_OK;
+  kivi::PackedQuantArgs a = {};
+  a.k = packed_rows(k);
+  a.v = packed_rows(v);
+  a.cu = cu_seqlens;
+  a.bt = c->block_table;
+  a.seq_lens = c->seq_lens;
+  a.k_res = c->k_res;
+  a.v_res = paged_vres(d, c);
+  a.k_codes = c->k_codes;
+  a.k_meta = c->k_meta;
+  a.v_codes = c->v_codes;
+  a.v_meta = c->v_meta;
+  a.num_pages = d->num_pages;
+  a.B = d->B;
+  a.Hkv = d->Hkv;
+  a.G = d->G;
+  a.bits = d->bits;
+  a.shift = page_shift_of(d->page_tokens);
+  a.max_pages = d->max_pages_per_seq;
+  a.T = (int)n_tokens;
+  return cuda_status(kivi::launch_packed_quantize(a, st));
+}
+
+// ------------------------------------------------------------------------------ pages
+size_t kivi_paged_pool_workspace_bytes(const kivi_paged_dims *d) {
+  if (check_paged_dims(d) != KIVI_OK || d->num_pages > (1 << 30)) return 0;
+  return pool_bytes(d);
+}
+
+int kivi_paged_reserve(const kivi_paged_dims *d, const kivi_paged_cache *c, const kivi_page_pool *p,
+                       const int32_t *extra, void *ws, size_t ws_bytes, cudaStream_t st) {
+  const int s = check_pool(d, c, p, extra, ws, ws_bytes);
+  if (s != KIVI_OK) return s;
+  kivi::PoolArgs a = pool_args(d, c, p, ws);
+  a.arg = extra;
+  return cuda_status(kivi::launch_pool_reserve(a, st));
+}
+
+int kivi_paged_reorder(const kivi_paged_dims *d, const kivi_paged_cache *c, const kivi_page_pool *p,
+                       const int32_t *parent, void *ws, size_t ws_bytes, cudaStream_t st) {
+  const int s = check_pool(d, c, p, parent, ws, ws_bytes);
+  if (s != KIVI_OK) return s;
+  kivi::PoolArgs a = pool_args(d, c, p, ws);
+  a.arg = parent;
+  return cuda_status(kivi::launch_pool_reorder(a, st));
+}
+
+int kivi_paged_compact(const kivi_paged_dims *d, const kivi_paged_cache *c, const kivi_page_pool *p,
+                       int32_t *new_ids, void *ws, size_t ws_bytes, cudaStream_t st) {
+  const int s = check_pool(d, c, p, new_ids, ws, ws_bytes);
+  if (s != KIVI_OK) return s;
+  kivi::PoolArgs a = pool_args(d, c, p, ws);
+  a.new_ids = new_ids;
+  return cuda_status(kivi::launch_pool_compact(a, st));
 }
 
 }  // extern "C"

@@ -192,6 +192,7 @@ struct PackedAttentionArgs {
   int Hq, Hkv;
   float softmax_scale;
 };
+bool packed_attention_fits(const PackedAttentionArgs &a);  // the launch's grid
 cudaError_t launch_packed_attention(const PackedAttentionArgs &a, cudaStream_t st);
 
 // The packed prompts quantized into the pages of their sequences.

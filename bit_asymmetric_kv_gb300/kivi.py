@@ -52,6 +52,14 @@ class kivi_paged_cache(ctypes.Structure):
                 ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p)]
 
 
+class kivi_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class kivi_page_pool(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("ref_counts", ctypes.c_void_p), ("info", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -94,6 +102,16 @@ def lib() -> ctypes.CDLL:
         L.kivi_paged_decode_step.argtypes = [PD, PC, P, P, P, i32, ctypes.c_float, P, P, sz, P]
         for name in ("kivi_paged_buffer_bytes", "kivi_paged_prefill", "kivi_paged_append_token",
                      "kivi_paged_decode_attention", "kivi_paged_decode_step"):
+            getattr(L, name).restype = ctypes.c_int
+        PR, PP = ctypes.POINTER(kivi_rows), ctypes.POINTER(kivi_page_pool)
+        L.kivi_prefill_attention_packed.argtypes = [i32, i32, i32, i32, P, i64, PR, PR, PR, ctypes.c_float, PR, P]
+        L.kivi_paged_prefill_packed.argtypes = [PD, PC, P, i64, PR, PR, P]
+        L.kivi_paged_pool_workspace_bytes.argtypes = [PD]
+        L.kivi_paged_pool_workspace_bytes.restype = sz
+        for name in ("kivi_paged_reserve", "kivi_paged_reorder", "kivi_paged_compact"):
+            getattr(L, name).argtypes = [PD, PC, PP, P, P, sz, P]
+        for name in ("kivi_prefill_attention_packed", "kivi_paged_prefill_packed", "kivi_paged_reserve",
+                     "kivi_paged_reorder", "kivi_paged_compact"):
             getattr(L, name).restype = ctypes.c_int
         L.kivi_status_string.argtypes = [ctypes.c_int]
         L.kivi_status_string.restype = ctypes.c_char_p
@@ -421,3 +439,148 @@ def kivi_paged_decode_step(cache: PagedCache, k_new: torch.Tensor, v_new: torch.
                                         _ptr(q), Hq, float(softmax_scale), _ptr(out), _ptr(ws),
                                         ws.numel() * ws.element_size(), _stream(stream)), "kivi_paged_decode_step")
     return out
+
+
+# ---------------------------------------------------------------------------------------
+# packed prompts, and pages handed out on the device
+# ---------------------------------------------------------------------------------------
+def _on(device: torch.device, stream):
+    """The stream of a call on `device`'s tensors, as a context that makes it the current one: the given
+    stream (a torch stream or a cudaStream_t), or the device's current one."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device) if int(stream) else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
+def _rows(t: torch.Tensor, name: str, device: torch.device) -> kivi_rows:
+    """kivi_rows of an fp16 CUDA tensor [tokens, heads, D] with contiguous channels.  The stride of an
+    axis of one element says nothing, and torch may hold any number there."""
+    if t.dtype != torch.float16 or not t.is_cuda or t.dim() != 3 or (t.numel() and t.stride(2) != 1):
+        raise TypeError(f"{name}: expected a CUDA float16 tensor [tokens, heads, D] with contiguous channels")
+    if t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}")
+    T, H, D = t.shape
+    return kivi_rows(t.data_ptr(), t.stride(0) if T > 1 else max(D, 128), t.stride(1) if H > 1 else max(D, 128))
+
+
+def _i32(t: torch.Tensor, name: str, numel: int, device: torch.device) -> torch.Tensor:
+    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.numel() != numel:
+        raise TypeError(f"{name}: expected a contiguous CUDA int32 tensor of {numel} elements")
+    if t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}")
+    return t
+
+
+def kivi_prefill_attention_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                                  softmax_scale: float, out: torch.Tensor | None = None,
+                                  stream=None) -> torch.Tensor:
+    """Causal attention of prompts packed into one token axis: q fp16 [T, Hq, D], k, v fp16 [T, Hkv, D] on
+    the device, any token and head strides that are multiples of 8 (views of one projection, or
+    transposed head-major tensors); sequence s is rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1
+    (int32 [n_seqs + 1] on the device).  Rows of no sequence are not written (zero in an `out` made
+    here)."""
+    dev = q.device
+    rq, rk, rv = _rows(q, "q", dev), _rows(k, "k", dev), _rows(v, "v", dev)
+    T, Hq, D = q.shape
+    if k.shape != v.shape or k.shape[0] != T or k.shape[2] != D:
+        raise ValueError(f"q {list(q.shape)}, k {list(k.shape)}, v {list(v.shape)} do not fit together")
+    if cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens holds at least two bounds")
+    _i32(cu_seqlens, "cu_seqlens", cu_seqlens.numel(), dev)
+    if out is not None and out.shape != q.shape:
+        raise ValueError(f"out: expected shape {list(q.shape)}")
+    with _on(dev, stream):
+        if out is None:
+            out = torch.zeros((T, Hq, D), dtype=torch.float16, device=dev)
+        ro = _rows(out, "out", dev)
+        if T:
+            _check(lib().kivi_prefill_attention_packed(Hq, k.shape[1], D, cu_seqlens.numel() - 1, _ptr(cu_seqlens), T,
+                                                       ctypes.byref(rq), ctypes.byref(rk), ctypes.byref(rv),
+                                                       float(softmax_scale), ctypes.byref(ro), _stream(None)),
+                   "kivi_prefill_attention_packed")
+    return out
+
+
+def kivi_paged_prefill_packed(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                              stream=None) -> None:
+    """Prompts of all sequences of a paged batch, packed: k, v fp16 [T, Hkv, D] (strides as for
+    kivi_prefill_attention_packed), cu_seqlens int32 [B + 1]; an empty sequence is left as it is."""
+    d, dev = cache.dims, cache.k_codes.device
+    rk, rv = _rows(k, "k", dev), _rows(v, "v", dev)
+    if k.shape != v.shape or tuple(k.shape[1:]) != (d.Hkv, d.D):
+        raise ValueError(f"k {list(k.shape)}, v {list(v.shape)}: expected [tokens, {d.Hkv}, {d.D}]")
+    _i32(cu_seqlens, "cu_seqlens", d.B + 1, dev)
+    if k.shape[0] == 0:
+        return
+    with _on(dev, stream):
+        _check(lib().kivi_paged_prefill_packed(ctypes.byref(d), ctypes.byref(cache.c), _ptr(cu_seqlens), k.shape[0],
+                                               ctypes.byref(rk), ctypes.byref(rv), _stream(None)),
+               "kivi_paged_prefill_packed")
+
+
+def kivi_paged_pool_workspace_bytes(dims: kivi_paged_dims) -> int:
+    return int(lib().kivi_paged_pool_workspace_bytes(ctypes.byref(dims)))
+
+
+@dataclass
+class PagePool:
+    """The reference counts of a paged cache's pages, what the last call did, and the workspace of the
+    page calls (include/kivi.h)."""
+
+    ref_counts: torch.Tensor  # int32 [num_pages]; a page is free when its count is not positive
+    info: torch.Tensor        # int32 [4]
+    ws: torch.Tensor          # uint8
+    c: kivi_page_pool
+
+    @classmethod
+    def allocate(cls, cache: PagedCache) -> "PagePool":
+        """A pool with every page free: the cache's block table is emptied."""
+        pool = cls.adopt(cache, torch.zeros(cache.dims.num_pages, dtype=torch.int32, device=cache.k_codes.device))
+        cache.block_table.fill_(-1)
+        return pool
+
+    @classmethod
+    def adopt(cls, cache: PagedCache, ref_counts: torch.Tensor, info: torch.Tensor | None = None) -> "PagePool":
+        """A pool over pages that the cache's block table holds already, with their counts."""
+        dev = cache.k_codes.device
+        nbytes = kivi_paged_pool_workspace_bytes(cache.dims)
+        if nbytes == 0:
+            raise KiviError(KIVI_ERR_UNSUPPORTED, "kivi_paged_pool_workspace_bytes")
+        _i32(ref_counts, "ref_counts", cache.dims.num_pages, dev)
+        if info is None:
+            info = torch.zeros(4, dtype=torch.int32, device=dev)
+        _i32(info, "info", 4, dev)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        c = kivi_page_pool(cache.block_table.data_ptr(), ref_counts.data_ptr(), info.data_ptr())
+        return cls(ref_counts, info, ws, c)
+
+
+def _pool_call(name: str, cache: PagedCache, pool: PagePool, array: torch.Tensor, what: str, numel: int,
+               stream) -> None:
+    dev = cache.k_codes.device
+    _i32(array, what, numel, dev)
+    with _on(dev, stream):
+        _check(getattr(lib(), name)(ctypes.byref(cache.dims), ctypes.byref(cache.c), ctypes.byref(pool.c),
+                                    _ptr(array), _ptr(pool.ws), pool.ws.numel(), _stream(None)), name)
+
+
+def kivi_paged_reserve(cache: PagedCache, pool: PagePool, extra: torch.Tensor, stream=None) -> None:
+    """Pages for extra[b] more tokens of every sequence b (int32 [B] on the device; <= 0: none)."""
+    _pool_call("kivi_paged_reserve", cache, pool, extra, "extra", cache.dims.B, stream)
+
+
+def kivi_paged_reorder(cache: PagedCache, pool: PagePool, parent: torch.Tensor, stream=None) -> None:
+    """Sequence b becomes what sequence parent[b] was (int32 [B] on the device; -1: empty)."""
+    _pool_call("kivi_paged_reorder", cache, pool, parent, "parent", cache.dims.B, stream)
+
+
+def kivi_paged_compact(cache: PagedCache, pool: PagePool, new_ids: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """Move the pages in use to the low ids; the new id of every page (int32 [num_pages], -1: free)."""
+    if new_ids is None:
+        with _on(cache.k_codes.device, stream):
+            new_ids = torch.empty_like(pool.ref_counts)
+    _pool_call("kivi_paged_compact", cache, pool, new_ids, "new_ids", cache.dims.num_pages, stream)
+    return new_ids

@@ -380,6 +380,123 @@ KIVI_API int kivi_paged_decode_step(const kivi_paged_dims *dims, const kivi_page
                                     float softmax_scale, uint16_t *out, void *ws, size_t ws_bytes,
                                     cudaStream_t stream);
 
+/*
+ * ---- Packed prompts ------------------------------------------------------------------
+ * Prompts of different lengths side by side in one token axis, as a serving engine
+ * admits them: sequence s is rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 of an axis of
+ * n_tokens rows.  cu_seqlens, int32 [n_seqs + 1], lives on the device; the host does not
+ * see the lengths, so the kernels guard them: a start is clamped to [0, n_tokens], an
+ * end to [start, n_tokens].  Sequences may be empty; rows of no sequence (padding
+ * behind the last one) are not used, whatever they hold, and not written.
+ * Sequences that overlap give unspecified results (no access outside the buffers).
+ *
+ * A tensor on that axis is kivi_rows: element (token, head, channel) is
+ * data[token * token_stride + head * head_stride + channel], strides in elements, so
+ * that the heads of one fused projection and head-major tensors are both taken as they
+ * are.  data is device memory, 16-byte aligned; strides are multiples of 8 elements
+ * (KIVI_ERR_ALIGN), at least D and at most 2^38 (KIVI_ERR_ARG, KIVI_ERR_UNSUPPORTED).
+ * n_seqs <= 512, n_tokens <= 2^31 - 1 (KIVI_ERR_UNSUPPORTED beyond).
+ */
+typedef struct {
+  uint16_t *data;        /* fp16; not written where the tensor is an input */
+  int64_t token_stride;
+  int64_t head_stride;
+} kivi_rows;
+
+/*
+ * Causal attention of every packed prompt over itself (section "Kod ve Entegrasyon
+ * Haritasi": the prompt's attention runs over its full-precision keys and values): for
+ * row i of a sequence, counted from its start, and query head h,
+ *   out_i = sum_{j <= i} softmax_j(softmax_scale * q_i . k_j) v_j
+ * over rows j of the same sequence, k and v of KV head h / (Hq / Hkv).  q, out: Hq
+ * heads; k, v: Hkv heads; Hq any multiple of Hkv; D = 128 (KIVI_ERR_UNSUPPORTED).
+ * The rows of a sequence must be finite; softmax_scale must be positive and finite
+ * (KIVI_ERR_ARG).  out's elements must not overlap one another (KIVI_ERR_ARG) or the
+ * inputs.  Scores, running maximum and sum, and the output's accumulators are fp32;
+ * the probabilities enter the P.V product in fp16.  n_tokens == 0 launches nothing.
+ * Nothing is allocated, and no state is kept between calls.
+ */
+KIVI_API int kivi_prefill_attention_packed(int32_t Hq, int32_t Hkv, int32_t D, int32_t n_seqs,
+                                           const int32_t *cu_seqlens, int64_t n_tokens, const kivi_rows *q,
+                                           const kivi_rows *k, const kivi_rows *v, float softmax_scale,
+                                           const kivi_rows *out, cudaStream_t stream);
+
+/*
+ * Quantize the packed prompts of a paged batch into their pages, sequence s of the pack
+ * into sequence s of the cache (n_seqs = dims->B), each as kivi_paged_prefill does for
+ * one: codes, scales, zeros and residual bit for bit, and seq_lens[s] = its length.  An
+ * empty sequence leaves sequence s of the cache as it is.  Tokens at or beyond
+ * max_pages_per_seq * P are dropped, and so are those of a position whose table entry
+ * lies outside the pool (the length still counts the latter).  Hkv <= 65535
+ * (KIVI_ERR_UNSUPPORTED).
+ */
+KIVI_API int kivi_paged_prefill_packed(const kivi_paged_dims *dims, const kivi_paged_cache *cache,
+                                       const int32_t *cu_seqlens, int64_t n_tokens, const kivi_rows *k,
+                                       const kivi_rows *v, cudaStream_t stream);
+
+/*
+ * ---- Pages handed out on the device ----------------------------------------------------
+ * A caller may assign pages itself, or leave it to the three calls below.  They keep one
+ * reference count per page beside the block table: a page is free when its count is not
+ * positive.  A table entry outside [0, num_pages) holds no page; the calls write -1.
+ * Start with every entry -1 and every count 0.  A caller that holds a page without
+ * a table entry (a shared prefix kept for later) adds one to its count.
+ * All three decide on the device from what is there (lengths, counts, table), always take
+ * the lowest free pages in the order of the sequences, and are asynchronous on the
+ * stream; a batch of them can be captured in a CUDA graph.  ws: device workspace of at
+ * least kivi_paged_pool_workspace_bytes(), 16-byte aligned, contents overwritten; calls
+ * that may overlap need one each.  num_pages <= 2^30 (KIVI_ERR_UNSUPPORTED).
+ */
+typedef struct {
+  int32_t *block_table;  /* the cache's (KIVI_ERR_ARG otherwise) */
+  int32_t *ref_counts;   /* [num_pages] device, 16-byte aligned */
+  int32_t *info;         /* [4] device: what the last call did, see below */
+} kivi_page_pool;
+
+/* Workspace bytes of the three calls, 0 on bad arguments.  Pure host arithmetic. */
+KIVI_API size_t kivi_paged_pool_workspace_bytes(const kivi_paged_dims *dims);
+
+/*
+ * Pages for tokens to come: every sequence b with extra[b] > 0 (int32 [B], device) gets a
+ * page in each table entry of positions 0 .. seq_lens[b] + extra[b] - 1 (at most the
+ * capacity) that holds none; its count becomes 1.  When the pool runs out, the entries
+ * left over, the last in (sequence, position) order, hold no page (tokens appended there
+ * are dropped).  info = {pages handed out, pages that were not there, pages in use
+ * afterwards, 0}.
+ */
+KIVI_API int kivi_paged_reserve(const kivi_paged_dims *dims, const kivi_paged_cache *cache,
+                                const kivi_page_pool *pool, const int32_t *extra, void *ws, size_t ws_bytes,
+                                cudaStream_t stream);
+
+/*
+ * Fork, free and reorder sequences: afterwards sequence b is what sequence parent[b] was
+ * before the call (int32 [B], device), and is empty when parent[b] is outside [0, B)
+ * (conventionally -1).  parent[b] = b leaves b alone; parent = a permutation with
+ * repetitions is a beam step.  The pages that are full are shared (their counts grow).
+ * Of the copies of one sequence s, the heir (s itself where parent[s] = s, else
+ * the lowest b) keeps its other pages too; every other copy gets a page of its own
+ * for the last, partly filled one, with the used rows copied, and none for reserved
+ * pages behind it.  The residual of a copy is copied.  Pages that no table entry holds any
+ * more are free at once, for the copies of the same call too.  When the pool runs
+ * out, the last copies (by b) end before their partly filled page: seq_lens is cut to
+ * whole pages.  info = {pages handed out, pages that were not there, pages in use
+ * afterwards, pages given back}.
+ */
+KIVI_API int kivi_paged_reorder(const kivi_paged_dims *dims, const kivi_paged_cache *cache,
+                                const kivi_page_pool *pool, const int32_t *parent, void *ws, size_t ws_bytes,
+                                cudaStream_t stream);
+
+/*
+ * Compact the pool: with L pages in use, those with ids >= L move into the free ids below
+ * L, lowest to lowest; the block table and the counts follow, and pages L .. num_pages - 1
+ * are free afterwards (their contents stay).  new_ids (int32 [num_pages], device) gets
+ * the new id of every page that was in use, -1 for the others.  info = {pages moved, 0,
+ * L, 0}.
+ */
+KIVI_API int kivi_paged_compact(const kivi_paged_dims *dims, const kivi_paged_cache *cache,
+                                const kivi_page_pool *pool, int32_t *new_ids, void *ws, size_t ws_bytes,
+                                cudaStream_t stream);
+
 /* Human-readable name of a kivi_status. */
 KIVI_API const char *kivi_status_string(int status);
 
