@@ -37,6 +37,8 @@
 #include <cuda.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "kivi_device.cuh"
 #include "kivi_internal.h"
 #include "kivi_packed.cuh"
@@ -538,6 +540,23 @@ int64_t grid_of(const PackedAttentionArgs &a) {
   return ((int64_t)a.T / (2 * kRows / pack) + a.n_seqs) * (a.Hq / pack);
 }
 
+// Once per device: the shared memory's limit, and that the kernel has the registers that the
+// warpgroups' split of them rests on.
+cudaError_t prepare_kernel() {
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (ready.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  cudaFuncAttributes f;
+  if ((e = cudaFuncGetAttributes(&f, packed_attention_kernel)) != cudaSuccess) return e;
+  if (f.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(packed_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 }  // namespace
 
 bool packed_attention_fits(const PackedAttentionArgs &a) { return grid_of(a) <= 0x7fffffff; }
@@ -548,12 +567,7 @@ cudaError_t launch_packed_attention(const PackedAttentionArgs &a, cudaStream_t s
   if (!encode(&maps.q, a.q, a.T, a.Hq, kRows / pack, pack) || !encode(&maps.k, a.k, a.T, a.Hkv, kRows, 1) ||
       !encode(&maps.v, a.v, a.T, a.Hkv, kRows, 1))
     return cudaErrorInvalidValue;
-  static const bool registers = [] {  // what the warpgroups' split of them rests on
-    cudaFuncAttributes f;
-    return cudaFuncGetAttributes(&f, packed_attention_kernel) == cudaSuccess && f.numRegs >= kLaunchRegs;
-  }();
-  if (!registers) return cudaErrorInvalidConfiguration;
-  cudaError_t e = cudaFuncSetAttribute(packed_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t e = prepare_kernel();
   if (e != cudaSuccess) return e;
   packed_attention_kernel<<<(unsigned)grid_of(a), kThreads, kSmem, st>>>(a, maps, pack);
   return cudaGetLastError();

@@ -444,9 +444,26 @@ def kivi_paged_decode_step(cache: PagedCache, k_new: torch.Tensor, v_new: torch.
 # ---------------------------------------------------------------------------------------
 # packed prompts, and pages handed out on the device
 # ---------------------------------------------------------------------------------------
-def _on(device: torch.device, stream):
-    """The stream of a call on `device`'s tensors, as a context that makes it the current one: the given
-    stream (a torch stream or a cudaStream_t), or the device's current one."""
+def _run(call: str, device: torch.device, stream, *args) -> None:
+    """Call `call` of the library with `device` current, on the given stream (a torch stream or a
+    cudaStream_t) or the device's current one.  Switching the device costs more than the call, so it is
+    switched only when it is not the current one."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device.index)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    fn = getattr(_lib or lib(), call)
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, int(stream))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, int(stream))
+    if status != KIVI_OK:
+        raise KiviError(status, call)
+
+
+def _allocating_on(device: torch.device, stream):
+    """Context in which tensors are made for use on the given stream."""
     if stream is None:
         stream = torch.cuda.current_stream(device)
     elif not hasattr(stream, "cuda_stream"):
@@ -457,20 +474,22 @@ def _on(device: torch.device, stream):
 def _rows(t: torch.Tensor, name: str, device: torch.device) -> kivi_rows:
     """kivi_rows of an fp16 CUDA tensor [tokens, heads, D] with contiguous channels.  The stride of an
     axis of one element says nothing, and torch may hold any number there."""
-    if t.dtype != torch.float16 or not t.is_cuda or t.dim() != 3 or (t.numel() and t.stride(2) != 1):
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not torch.float16 or not t.is_cuda or len(shape) != 3 or (stride[2] != 1 and t.numel()):
         raise TypeError(f"{name}: expected a CUDA float16 tensor [tokens, heads, D] with contiguous channels")
     if t.device != device:
         raise ValueError(f"{name}: expected a tensor on {device}")
-    T, H, D = t.shape
-    return kivi_rows(t.data_ptr(), t.stride(0) if T > 1 else max(D, 128), t.stride(1) if H > 1 else max(D, 128))
+    T, H, D = shape
+    return kivi_rows(t.data_ptr(), stride[0] if T > 1 else max(D, 128), stride[1] if H > 1 else max(D, 128))
 
 
-def _i32(t: torch.Tensor, name: str, numel: int, device: torch.device) -> torch.Tensor:
-    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.numel() != numel:
+def _i32(t: torch.Tensor, name: str, numel: int, device: torch.device) -> int:
+    """Address of a contiguous int32 tensor of `numel` elements on `device`."""
+    if t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous() or t.numel() != numel:
         raise TypeError(f"{name}: expected a contiguous CUDA int32 tensor of {numel} elements")
     if t.device != device:
         raise ValueError(f"{name}: expected a tensor on {device}")
-    return t
+    return t.data_ptr()
 
 
 def kivi_prefill_attention_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -483,23 +502,23 @@ def kivi_prefill_attention_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Ten
     here)."""
     dev = q.device
     rq, rk, rv = _rows(q, "q", dev), _rows(k, "k", dev), _rows(v, "v", dev)
-    T, Hq, D = q.shape
-    if k.shape != v.shape or k.shape[0] != T or k.shape[2] != D:
-        raise ValueError(f"q {list(q.shape)}, k {list(k.shape)}, v {list(v.shape)} do not fit together")
-    if cu_seqlens.numel() < 2:
+    shape, kv = q.shape, k.shape
+    T, Hq, D = shape
+    if kv != v.shape or kv[0] != T or kv[2] != D:
+        raise ValueError(f"q {list(shape)}, k {list(kv)}, v {list(v.shape)} do not fit together")
+    bounds = cu_seqlens.numel()
+    if bounds < 2:
         raise ValueError("cu_seqlens holds at least two bounds")
-    _i32(cu_seqlens, "cu_seqlens", cu_seqlens.numel(), dev)
-    if out is not None and out.shape != q.shape:
-        raise ValueError(f"out: expected shape {list(q.shape)}")
-    with _on(dev, stream):
-        if out is None:
-            out = torch.zeros((T, Hq, D), dtype=torch.float16, device=dev)
-        ro = _rows(out, "out", dev)
-        if T:
-            _check(lib().kivi_prefill_attention_packed(Hq, k.shape[1], D, cu_seqlens.numel() - 1, _ptr(cu_seqlens), T,
-                                                       ctypes.byref(rq), ctypes.byref(rk), ctypes.byref(rv),
-                                                       float(softmax_scale), ctypes.byref(ro), _stream(None)),
-                   "kivi_prefill_attention_packed")
+    cu = _i32(cu_seqlens, "cu_seqlens", bounds, dev)
+    if out is None:
+        with _allocating_on(dev, stream):
+            out = torch.zeros(shape, dtype=torch.float16, device=dev)
+    elif out.shape != shape:
+        raise ValueError(f"out: expected shape {list(shape)}")
+    ro = _rows(out, "out", dev)
+    if T:
+        _run("kivi_prefill_attention_packed", dev, stream, Hq, kv[1], D, bounds - 1, cu, T, rq, rk, rv,
+             float(softmax_scale), ro)
     return out
 
 
@@ -511,13 +530,9 @@ def kivi_paged_prefill_packed(cache: PagedCache, k: torch.Tensor, v: torch.Tenso
     rk, rv = _rows(k, "k", dev), _rows(v, "v", dev)
     if k.shape != v.shape or tuple(k.shape[1:]) != (d.Hkv, d.D):
         raise ValueError(f"k {list(k.shape)}, v {list(v.shape)}: expected [tokens, {d.Hkv}, {d.D}]")
-    _i32(cu_seqlens, "cu_seqlens", d.B + 1, dev)
-    if k.shape[0] == 0:
-        return
-    with _on(dev, stream):
-        _check(lib().kivi_paged_prefill_packed(ctypes.byref(d), ctypes.byref(cache.c), _ptr(cu_seqlens), k.shape[0],
-                                               ctypes.byref(rk), ctypes.byref(rv), _stream(None)),
-               "kivi_paged_prefill_packed")
+    cu = _i32(cu_seqlens, "cu_seqlens", d.B + 1, dev)
+    if k.shape[0]:
+        _run("kivi_paged_prefill_packed", dev, stream, d, cache.c, cu, k.shape[0], rk, rv)
 
 
 def kivi_paged_pool_workspace_bytes(dims: kivi_paged_dims) -> int:
@@ -560,10 +575,8 @@ class PagePool:
 def _pool_call(name: str, cache: PagedCache, pool: PagePool, array: torch.Tensor, what: str, numel: int,
                stream) -> None:
     dev = cache.k_codes.device
-    _i32(array, what, numel, dev)
-    with _on(dev, stream):
-        _check(getattr(lib(), name)(ctypes.byref(cache.dims), ctypes.byref(cache.c), ctypes.byref(pool.c),
-                                    _ptr(array), _ptr(pool.ws), pool.ws.numel(), _stream(None)), name)
+    at = _i32(array, what, numel, dev)
+    _run(name, dev, stream, cache.dims, cache.c, pool.c, at, pool.ws.data_ptr(), pool.ws.numel())
 
 
 def kivi_paged_reserve(cache: PagedCache, pool: PagePool, extra: torch.Tensor, stream=None) -> None:
@@ -580,7 +593,7 @@ def kivi_paged_compact(cache: PagedCache, pool: PagePool, new_ids: torch.Tensor 
                        stream=None) -> torch.Tensor:
     """Move the pages in use to the low ids; the new id of every page (int32 [num_pages], -1: free)."""
     if new_ids is None:
-        with _on(cache.k_codes.device, stream):
+        with _allocating_on(cache.k_codes.device, stream):
             new_ids = torch.empty_like(pool.ref_counts)
     _pool_call("kivi_paged_compact", cache, pool, new_ids, "new_ids", cache.dims.num_pages, stream)
     return new_ids
