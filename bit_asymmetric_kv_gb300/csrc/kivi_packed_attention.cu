@@ -142,36 +142,133 @@ __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
-// arrives on the barrier when every MMA issued so far by this thread is done
-__device__ __forceinline__ void tc_commit(uint64_t *b) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_u32(b))
-               : "memory");
+// The MMA warp runs converged, so that addresses and descriptors stay in uniform
+// registers; only the instructions themselves are one lane's (`one` is 1 in it, else 0).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one;
+}
+// arrives on the barrier when every MMA issued so far by the lane is done
+__device__ __forceinline__ void tc_commit(uint64_t *b, uint32_t one) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n"
+      " @p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(b)),
+      "r"(one)
+      : "memory");
 }
 
-// Shared-memory descriptor of a tile half, 128-byte swizzle: addresses in 16-byte units,
-// lead at bits 16-29, stride at 32-45 (8 rows of 128 bytes: 1024 bytes).  With the
-// contraction along the rows' bytes (Q, K) lead is not used; with it along the rows
-// (V) lead is the distance between the two 64-channel halves.
-__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t lead) {
-  return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         (1ull << 46) | (2ull << 61);
-}
+// Shared-memory descriptor of a tile half, 128-byte swizzle: addresses in 16-byte units
+// in the low word, lead at bits 16-29, stride (8 rows of 128 bytes: 1024 bytes) at 32-45,
+// version and swizzle above.  With the contraction along the rows' bytes (Q, K) lead is
+// not used; with it along the rows (V) lead is the distance between the two 64-channel halves.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) { return (addr >> 4) | ((lead >> 4) << 16); }
+constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
 // Instruction descriptor: fp32 accumulators (bit 4), fp16 operands, B's major axis (bit
 // 16: 1 when its rows are the contraction), N / 8 at 17, M / 16 at 24.
 constexpr uint32_t kIdescQK = (1u << 4) | ((kRows / 8) << 17) | ((kRows / 16) << 24);
 constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((kD / 8) << 17) | ((kRows / 16) << 24);
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// The eight MMAs of a 128 x 128 x 128 product, 16 of the contraction each, by the lane with
+// `one` set.  Both operands in shared memory, contraction along the rows' bytes: 32 bytes a
+// step, then the other half.  acc: add to what the accumulators hold.
+__device__ __forceinline__ void mma_qk(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t one) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "{\n"
+      " .reg .pred p, q, t;\n"
+      " .reg .b32 x, y;\n"
+      " .reg .b64 a, b;\n"
+      " setp.ne.u32 p, %6, 0;\n"
+      " setp.ne.u32 q, %5, 0;\n"
+      " setp.eq.u32 t, 0, 0;\n"
+      " add.u32 x, %1, 0;\n"
+      " mov.b64 a, {x, %4};\n"
+      " add.u32 y, %2, 0;\n"
+      " mov.b64 b, {y, %4};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n"
+      " add.u32 x, %1, 2;\n"
+      " mov.b64 a, {x, %4};\n"
+      " add.u32 y, %2, 2;\n"
+      " mov.b64 b, {y, %4};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.u32 x, %1, 4;\n"
+      " mov.b64 a, {x, %4};\n"
+      " add.u32 y, %2, 4;\n"
+      " mov.b64 b, {y, %4};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.u32 x, %1, 6;\n"
+      " mov.b64 a, {x, %4};\n"
+      " add.u32 y, %2, 6;\n"
+      " mov.b64 b, {y, %4};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.u32 x, %1, 1024;\n"
+      " mov.b64 a, {x, %4};\n"
+      " add.u32 y, %2, 1024;\n"
+      " mov.b64 b, {y, %4};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.u32 x, %1, 1026;\n"
+      " mov.b64 a, {x, %4};\n"
+      " add.u32 y, %2, 1026;\n"
+      " mov.b64 b, {y, %4};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.u32 x, %1, 1028;\n"
+      " mov.b64 a, {x, %4};\n"
+      " add.u32 y, %2, 1028;\n"
+      " mov.b64 b, {y, %4};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.u32 x, %1, 1030;\n"
+      " mov.b64 a, {x, %4};\n"
+      " add.u32 y, %2, 1030;\n"
+      " mov.b64 b, {y, %4};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      "}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(kDescHi), "r"(acc), "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+// A in tensor memory (16 fp16 are 8 columns), B's contraction along the rows: 16 rows a step.
+__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t one) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
-          d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "{\n"
+      " .reg .pred p, q, t;\n"
+      " .reg .b32 x, y;\n"
+      " .reg .b64 a, b;\n"
+      " setp.ne.u32 p, %6, 0;\n"
+      " setp.ne.u32 q, %5, 0;\n"
+      " setp.eq.u32 t, 0, 0;\n"
+      " add.u32 x, %1, 0;\n"
+      " add.u32 y, %2, 0;\n"
+      " mov.b64 b, {y, %4};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, q;\n"
+      " add.u32 x, %1, 8;\n"
+      " add.u32 y, %2, 128;\n"
+      " mov.b64 b, {y, %4};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n"
+      " add.u32 x, %1, 16;\n"
+      " add.u32 y, %2, 256;\n"
+      " mov.b64 b, {y, %4};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n"
+      " add.u32 x, %1, 24;\n"
+      " add.u32 y, %2, 384;\n"
+      " mov.b64 b, {y, %4};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n"
+      " add.u32 x, %1, 32;\n"
+      " add.u32 y, %2, 512;\n"
+      " mov.b64 b, {y, %4};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n"
+      " add.u32 x, %1, 40;\n"
+      " add.u32 y, %2, 640;\n"
+      " mov.b64 b, {y, %4};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n"
+      " add.u32 x, %1, 48;\n"
+      " add.u32 y, %2, 768;\n"
+      " mov.b64 b, {y, %4};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n"
+      " add.u32 x, %1, 56;\n"
+      " add.u32 y, %2, 896;\n"
+      " mov.b64 b, {y, %4};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n"
+      "}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(kDescHi), "r"(acc), "r"(one)
       : "memory");
 }
 
@@ -255,57 +352,73 @@ __device__ __forceinline__ void load_role(const Maps &maps, const Work &w, Bars 
 
 // -------------------------------------------------------------------------- products
 __device__ __forceinline__ void mma_role(const Work &w, Bars &sh) {
+  const uint32_t one = elect_one();
   bool ok = true;
-  auto qk = [&](int x, int c) {  // scores of tile x with the K tile of copy c
-    const uint32_t q = w.sQ + x * kTileBytes, k = w.sKV + (c % kStages) * kTileBytes;
-#pragma unroll
-    for (int kk = 0; kk < kD / 16; ++kk) {
-      const uint32_t off = (kk / 4) * kHalfBytes + (kk % 4) * 32;
-      mma_ss(w.tmem + x * kRows, tile_desc(q + off, 16), tile_desc(k + off, 16), kIdescQK, kk > 0);
-    }
-    tc_commit(&sh.s[x]);
+  const uint32_t q0 = desc_lo(w.sQ, 16), k0 = desc_lo(w.sKV, 16), v0 = desc_lo(w.sKV, kHalfBytes);
+  constexpr uint32_t kTile16 = kTileBytes >> 4;
+  auto wait = [&](uint64_t *b, uint32_t parity) { return __all_sync(0xffffffffu, bar_wait(b, parity, &sh.abort)) != 0; };
+  auto qk = [&](int x, int st) {  // scores of tile x with the K tile in stage st
+    mma_qk(w.tmem + x * kRows, q0 + x * kTile16, k0 + st * kTile16, kIdescQK, 0, one);
+    tc_commit(&sh.s[x], one);
   };
-  auto pv = [&](int x, int c, bool acc) {  // output of tile x with the V tile of copy c
-    const uint32_t v = w.sKV + (c % kStages) * kTileBytes;
-#pragma unroll
-    for (int kk = 0; kk < kRows / 16; ++kk)
-      mma_ts(w.tmem + 2 * kRows + x * kD, w.tmem + x * kRows + kk * 8, tile_desc(v + kk * 2048, kHalfBytes), kIdescPV,
-             acc || kk > 0);
-    tc_commit(&sh.o[x]);
+  auto pv = [&](int x, int st, bool acc) {  // output of tile x with the V tile in stage st
+    mma_pv(w.tmem + 2 * kRows + x * kD, w.tmem + x * kRows, v0 + st * kTile16, kIdescPV, acc, one);
+    tc_commit(&sh.o[x], one);
   };
   // A stage is handed back only where a later copy waits for it: no arrival is left over
   // when the CTA ends.
-  auto give = [&](int c) {
-    if (c + kStages < 2 * w.n) tc_commit(&sh.empty[c % kStages]);
+  auto give = [&](int c, int st) {
+    if (c + kStages < 2 * w.n) tc_commit(&sh.empty[st], one);
   };
-  int done[2] = {0, 0};  // P.V products of each tile
-  for (int x = 0; x < 2 && ok; ++x)
-    if (w.on[x]) ok = bar_wait(&sh.q[x], 0, &sh.abort);
-  ok = ok && bar_wait(&sh.full[0], 0, &sh.abort);
+  const int nt0 = w.nt[0], nt1 = w.nt[1];
+  int done0 = 0, done1 = 0;  // P.V products of each tile
+  ok = wait(&sh.q[0], 0);
+  if (ok && nt1) ok = wait(&sh.q[1], 0);
+  ok = ok && wait(&sh.full[0], 0);
   tc_fence_after();
-  for (int x = 0; x < 2 && ok; ++x)
-    if (w.n - 1 < w.nt[x]) qk(x, 0);
-  if (ok) give(0);
-  if (ok && w.tail < kRows) ok = bar_wait(&sh.zeroed, 0, &sh.abort);
+  if (ok) {
+    if (w.n <= nt0) qk(0, 0);
+    if (w.n <= nt1) qk(1, 0);
+    give(0, 0);
+    if (w.tail < kRows) ok = wait(&sh.zeroed, 0);
+  }
+  int sv = 1, sk = 2, cv = 1;       // stages of V of pass i and K of pass i + 1; copy of the former
+  uint32_t pv_par = 0, pk_par = 0;  // and their phases
   for (int i = 0; i < w.n && ok; ++i) {
-    const int cv = 2 * i + 1, ck = 2 * i + 2;
-    const bool more = i + 1 < w.n;
-    ok = bar_wait(&sh.full[cv % kStages], (cv / kStages) & 1, &sh.abort);
-    if (ok && more) ok = bar_wait(&sh.full[ck % kStages], (ck / kStages) & 1, &sh.abort);
-    for (int x = 0; x < 2 && ok; ++x) {
-      if (w.n - 1 - i < w.nt[x]) {
-        ok = bar_wait(&sh.p[x], done[x] & 1, &sh.abort);
-        if (!ok) break;
-        tc_fence_after();
-        pv(x, cv, done[x] > 0);
-        ++done[x];
-      }
-      // the scores go where the probabilities were: MMAs run in the order of issue
-      if (more && w.n - 2 - i < w.nt[x]) qk(x, ck);
+    const int left = w.n - 1 - i;  // key tile of this pass
+    const bool more = left > 0;
+    ok = wait(&sh.full[sv], pv_par);
+    if (ok && left < nt0) {
+      ok = wait(&sh.p[0], done0 & 1);
+      if (!ok) break;
+      tc_fence_after();
+      pv(0, sv, done0 > 0);
+      ++done0;
     }
-    if (ok) {
-      give(cv);
-      give(ck);
+    if (ok && more) ok = wait(&sh.full[sk], pk_par);
+    if (!ok) break;
+    // the scores go where the probabilities were: MMAs run in the order of issue
+    if (more && left - 1 < nt0) qk(0, sk);
+    if (left < nt1) {
+      ok = wait(&sh.p[1], done1 & 1);
+      if (!ok) break;
+      tc_fence_after();
+      pv(1, sv, done1 > 0);
+      ++done1;
+    }
+    give(cv, sv);
+    if (more && left - 1 < nt1) qk(1, sk);
+    give(cv + 1, sk);
+    cv += 2;
+    sv += 2;
+    if (sv >= kStages) {
+      sv -= kStages;
+      pv_par ^= 1;
+    }
+    sk += 2;
+    if (sk >= kStages) {
+      sk -= kStages;
+      pk_par ^= 1;
     }
   }
 }
@@ -482,8 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (warp == kLoadWarp) {
         load_role(maps, w, sh, lane);
       } else if (warp == kMmaWarp) {
-        if (lane == 0) mma_role(w, sh);
-        __syncwarp();
+        mma_role(w, sh);
       }
     } else {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
