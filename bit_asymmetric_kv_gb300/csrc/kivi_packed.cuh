@@ -25,68 +25,87 @@ __device__ __forceinline__ void packed_bounds(const int32_t *cu, int s, int T, i
   *len = min(max(__ldg(cu + s + 1), a), T) - a;
 }
 
-// Block `idx` of all sequences' blocks of `bt` rows, longest first: the blocks of
-// level L (the L-th of their sequence, whose causal rows see L + 1 blocks of keys) come
-// before those of level L - 1, and within a level in the order of the sequences.
-// f(L) = sum_s max(0, blocks_s - L) blocks have level L or more, so the level of `idx`
-// is the largest L with f(L) > idx: a binary search, each step one sum over the warp.
-// Every lane of a warp calls it; false when there is no such block (or the bounds
-// overlap so that the sums overflow: nothing outside a sequence is ever returned).
-__device__ __forceinline__ bool packed_block(const int32_t *cu, int n_seqs, int T, int bt, unsigned idx,
-                                             PackedBlock *out) {
-  const int lane = threadIdx.x & 31;
-  int nb[kPackedMaxSeqs / 32];
-  int most = 0;
+// All sequences' blocks of `bt` rows, longest first: the blocks of level L (the L-th of
+// their sequence, whose causal rows see L + 1 blocks of keys) come before those of level
+// L - 1.  With the sequences sorted by their number of blocks, nb_1 >= nb_2 >= ..., the
+// levels from nb_{j+1} to nb_j - 1 have one block of each of the first j sequences, and
+//   C_j = sum_{i <= j} (nb_i - nb_j)
+// blocks come before them, so that block `item` is found by a binary search in C and one
+// division.  Kept in shared memory, built once by a CTA.
+struct PackedList {
+  int nb[kPackedMaxSeqs];             // blocks of the j-th longest sequence
+  int before[kPackedMaxSeqs];         // C_j
+  int start[kPackedMaxSeqs], len[kPackedMaxSeqs];  // by sequence, as given
+  int work[kPackedMaxSeqs];           // blocks by sequence, as given
+  uint16_t order[kPackedMaxSeqs];     // sequence of rank j
+  int n, total;
+
+  // Every thread of the CTA calls it; synchronises.
+  __device__ __forceinline__ void build(const int32_t *cu, int n_seqs, int T, int bt) {
+    const int tid = threadIdx.x;
+    for (int s = tid; s < n_seqs; s += blockDim.x) {
+      int a, m;
+      packed_bounds(cu, s, T, &a, &m);
+      start[s] = a;
+      len[s] = m;
+      work[s] = m / bt + (m % bt != 0);
+    }
+    __syncthreads();
+    for (int s = tid; s < n_seqs; s += blockDim.x) {
+      const int mine = work[s];
+      int rank = 0;
+#pragma unroll 8
+      for (int o = 0; o < n_seqs; ++o) {
+        const int other = work[o];
+        rank += other > mine || (other == mine && o < s);
+      }
+      nb[rank] = mine;
+      order[rank] = (uint16_t)s;
+    }
+    __syncthreads();
+    if (tid < 32) {
+      // sums up to each rank, 32 at a time; bounds that overlap may pass any count: cut at
+      // what lengths that do not overlap can reach
+      const int64_t most = (int64_t)T / bt + n_seqs;
+      int64_t carry = 0;
+      for (int j0 = 0; j0 < n_seqs; j0 += 32) {
+        const int j = j0 + tid, mine = j < n_seqs ? nb[j] : 0;
+        int64_t sum = mine;
 #pragma unroll
-  for (int k = 0; k < kPackedMaxSeqs / 32; ++k) {
-    nb[k] = 0;
-    if (32 * k < n_seqs) {
-      const int s = 32 * k + lane;
-      if (s < n_seqs) {
-        int start, len;
-        packed_bounds(cu, s, T, &start, &len);
-        nb[k] = len / bt + (len % bt != 0);
-        most = max(most, nb[k]);
+        for (int off = 1; off < 32; off <<= 1) {
+          const int64_t o = __shfl_up_sync(0xffffffffu, sum, off);
+          if (tid >= off) sum += o;
+        }
+        sum += carry;
+        if (j < n_seqs) before[j] = (int)min(most, sum - (int64_t)(j + 1) * mine);
+        carry = __shfl_sync(0xffffffffu, sum, 31);
+      }
+      if (tid == 0) {
+        n = n_seqs;
+        total = (int)min(most, carry);
       }
     }
+    __syncthreads();
   }
-  most = __reduce_max_sync(0xffffffffu, most);
-  auto f = [&](int L) {
-    unsigned c = 0;
-#pragma unroll
-    for (int k = 0; k < kPackedMaxSeqs / 32; ++k)
-      if (32 * k < n_seqs) c += (unsigned)max(nb[k] - L, 0);
-    return __reduce_add_sync(0xffffffffu, c);
-  };
-  if (most == 0 || f(0) <= idx) return false;
-  int lo = 0, hi = most;  // f(lo) > idx >= f(hi)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (f(mid) > idx)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  unsigned rank = idx - f(lo + 1);  // among the sequences with more than lo blocks
-  int found = -1;
-#pragma unroll
-  for (int k = 0; k < kPackedMaxSeqs / 32; ++k) {
-    if (32 * k < n_seqs) {
-      const uint32_t m = __ballot_sync(0xffffffffu, nb[k] > lo);
-      const unsigned c = __popc(m);
-      if (found < 0) {
-        if (rank < c)
-          found = 32 * k + (int)__fns(m, 0, (int)rank + 1);
-        else
-          rank -= c;
-      }
+
+  // Block `item` < total.
+  __device__ __forceinline__ PackedBlock find(unsigned item) const {
+    int lo = 0, hi = n;  // before[lo] <= item < before[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((unsigned)before[mid] <= item)
+        lo = mid;
+      else
+        hi = mid;
     }
+    const unsigned rest = item - before[lo], width = lo + 1, down = rest / width;
+    PackedBlock b;
+    b.seq = order[rest - down * width];
+    b.start = start[b.seq];
+    b.len = len[b.seq];
+    b.level = max(nb[lo] - 1 - (int)down, 0);
+    return b;
   }
-  if (found < 0 || found >= n_seqs) return false;
-  out->seq = found;
-  packed_bounds(cu, found, T, &out->start, &out->len);
-  out->level = lo;
-  return (int64_t)lo * bt < out->len;
-}
+};
 
 }  // namespace kivi

@@ -5,21 +5,24 @@
 // head h / (Hq / Hkv):
 //   out_i = sum_{j <= i} softmax_j(sigma q_i . k_j) v_j,   j over the same sequence.
 //
-// One CTA takes two tiles, A and B, of 128 query rows, and walks the keys and values
-// in tiles of 128 rows from the diagonal down to the sequence's first.  A query tile is
-// 128 / P consecutive tokens of P query heads that read the same KV head, P the
+// A block of work is two tiles, A and B, of 128 query rows, which walk the keys and
+// values in tiles of 128 rows from the diagonal down to the sequence's first.  A query
+// tile is 128 / P consecutive tokens of P query heads that read the same KV head, P the
 // largest power of two (up to 16) that divides Hq / Hkv: the heads of a group share every
-// key and value tile, and a short prompt wastes fewer rows of a tile.
+// key and value tile, and a short prompt wastes fewer rows of a tile.  One CTA per SM
+// takes block after block, longest first, so that the next block's copies and first
+// products run under the last one's output.
 //
-// Roles (12 warps, the last two idle):
+// Roles (12 warps):
 //   warps 0-3, 4-7  softmax of tile A, of tile B: a thread holds one row.  It reads the 128
 //                   scores from tensor memory, keeps the running maximum and sum, and
-//                   writes the probabilities over the scores, as fp16.
-//   warp 8          one lane issues the MMAs: S = Q K^T (both operands in shared memory) and
-//                   O += P V (P in tensor memory), tile A and B in turn, so that one
-//                   tile's softmax runs under the other's MMAs.
-//   warp 9          one lane issues the tensor-map copies: Q once, K and V tiles through a
-//                   ring of stages.
+//                   writes the probabilities over the scores, as fp16; at the end of a
+//                   block it divides the output by the sum and stores it.
+//   warps 8, 9      one lane issues the MMAs of tile A, of tile B: S = Q K^T (both operands in
+//                   shared memory) and O += P V (P in tensor memory); one tile's softmax
+//                   runs under the other's MMAs.
+//   warp 10         one lane issues the tensor-map copies: Q, and K and V tiles through a
+//                   ring of stages.  (Warp 11 is idle: registers go by four warps.)
 // Tensor memory: S/P of A and B (128 columns each), O of A and B (128 each): all 512.
 //
 // The maximum that the probabilities are relative to may lag behind the true one by 2^8:
@@ -30,13 +33,14 @@
 //
 // Rows behind a sequence's end share its last tiles.  As query rows they are computed and
 // not stored; as keys they are masked by causality; as values they would meet
-// probability 0, and a NaN there would spread, so warp 9 overwrites them with zeros.
+// probability 0, and a NaN there would spread, so the MMA warps overwrite them with zeros first.
 //
 // Every wait is bounded: one that runs out (a copy that never completes) ends all roles
-// of the CTA, whose rows are then NaN.
+// of the CTA, whose rows from then on are NaN.
 #include <cuda.h>
 #include <math.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "kivi_device.cuh"
@@ -49,14 +53,14 @@ namespace {
 
 constexpr int kRows = 128;                  // query rows of a tile, keys of a tile
 constexpr int kThreads = 384;               // three warpgroups
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kMmaWarp = 8, kLoadWarp = 10;  // two MMA warps, one a tile
 // Registers a thread: the CTA's share at launch, and how the warpgroups split it (a
 // softmax thread holds a row of 128 scores).
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "more registers than the CTA was launched with");
 constexpr int kTileBytes = kRows * kD * 2;  // 32 KB: two halves of 64 channels
 constexpr int kHalfBytes = kTileBytes / 2;  // 128 rows of 128 bytes, 128-byte swizzle
-constexpr int kStages = 5;                  // K and V tiles in flight
+constexpr int kStages = 4;                  // K and V tiles in flight
 constexpr int kMaxPack = 16;
 constexpr float kLag = 8.f;                 // log2 by which the reference maximum may lag
 constexpr float kShift = 7.f;               // log2 of the probabilities' scale
@@ -64,18 +68,18 @@ constexpr float kLog2eP = 1.4426950408889634f;
 constexpr int kPolls = 1 << 22;             // of a wait, each suspended by the hardware for a while
 constexpr uint32_t kTmemCols = 512;
 
-struct __align__(8) Bars {
-  uint64_t q[2];           // Q tile landed
-  uint64_t full[kStages];  // K or V tile landed
-  uint64_t empty[kStages]; // the MMAs that read it are done
-  uint64_t s[2];           // scores of a tile written
-  uint64_t p[2];           // its probabilities written
-  uint64_t o[2];           // its P.V done
-  uint64_t zeroed;         // value rows behind the sequence overwritten
+struct __align__(16) Bars {
+  uint64_t q[2];            // Q tile landed
+  uint64_t q_free[2];       // the block's last scores of it are done
+  uint64_t full[kStages];   // K or V tile landed
+  uint64_t empty[kStages];  // both tiles are through with it
+  uint64_t s[2];            // scores of a tile written
+  uint64_t p[2][2];         // the probabilities of its first, its second 64 keys written
+  uint64_t o[2][2];         // their P.V done
+  uint64_t zeroed;          // value rows behind the sequence overwritten, for tile A
   uint32_t tmem;
   int abort;
-  int found;
-  PackedBlock blk;
+  PackedList list;
 };
 constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + (int)sizeof(Bars);
 static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
@@ -84,20 +88,46 @@ struct Maps {
   CUtensorMap q, k, v;
 };
 
-// What the roles of a CTA work on.
-struct Work {
-  unsigned char *tiles;  // Q of A, Q of B, the stages
+// What the roles of a CTA share.
+struct Cta {
+  unsigned char *tiles;   // Q of A, Q of B, the stages
   uint32_t sQ, sKV;
   uint32_t tmem;
-  int start, len;        // the sequence
-  int head0, kvh;
-  int tpt;               // tokens of a query tile
-  int base[2];           // first token of A, of B
-  bool on[2];
-  int nt[2];             // key tiles, the last one on the diagonal
-  int n;                 // passes: pass i works on key tile n - 1 - i
-  int tail;              // rows of the last key tile inside the sequence (more than a tile: all)
+  int tpt;                // tokens of a query tile
+  unsigned hgroups;       // head groups that share a tile
+  int heads_per_kv, pack;
+  int64_t items;          // blocks of all sequences and head groups
 };
+
+// One block of work.
+struct Block {
+  int start, len;         // the sequence
+  int head0, kvh;
+  int base0, base1;       // first token of A, of B
+  int nt0, nt1;           // key tiles of each, the last one on the diagonal (B: 0 when it has no row)
+  int n;                  // passes: pass i works on key tile n - 1 - i
+  int tail;               // rows of the last key tile inside the sequence (more than a tile: all)
+};
+
+// Block k of this CTA: the list is dealt out back and forth, so that the first CTAs do not
+// get the longer block of every round.
+__device__ __forceinline__ bool block_of(const Cta &c, const PackedList &list, int k, Block *w) {
+  const int64_t G = gridDim.x, at = k * G + ((k & 1) ? G - 1 - blockIdx.x : blockIdx.x);
+  if (at >= c.items) return false;
+  const unsigned item = (unsigned)(at / c.hgroups), hg = (unsigned)(at - (int64_t)item * c.hgroups);
+  const PackedBlock b = list.find(item);
+  w->start = b.start;
+  w->len = b.len;
+  w->head0 = (int)hg * c.pack;
+  w->kvh = w->head0 / c.heads_per_kv;
+  w->base0 = b.level * 2 * c.tpt;
+  w->base1 = w->base0 + c.tpt;
+  w->nt0 = w->base0 / kRows + 1;
+  w->nt1 = w->base1 < w->len ? w->base1 / kRows + 1 : 0;
+  w->n = max(w->nt0, w->nt1);
+  w->tail = w->len - (w->n - 1) * kRows;
+  return true;
+}
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -225,13 +255,14 @@ __device__ __forceinline__ void mma_qk(uint32_t d, uint32_t a, uint32_t b, uint3
       "r"(a), "r"(b), "r"(idesc), "r"(kDescHi), "r"(acc), "r"(one)
       : "memory");
 }
-// A in tensor memory (16 fp16 are 8 columns), B's contraction along the rows: 16 rows a step.
+// Four MMAs of a 128 x 64 x 128 product: A in tensor memory (16 fp16 are 8 columns), B's
+// contraction along the rows, 16 rows a step.
 __device__ __forceinline__ void mma_pv(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc, uint32_t one) {
   asm volatile(
       "{\n"
       " .reg .pred p, q, t;\n"
       " .reg .b32 x, y;\n"
-      " .reg .b64 a, b;\n"
+      " .reg .b64 b;\n"
       " setp.ne.u32 p, %6, 0;\n"
       " setp.ne.u32 q, %5, 0;\n"
       " setp.eq.u32 t, 0, 0;\n"
@@ -249,22 +280,6 @@ __device__ __forceinline__ void mma_pv(uint32_t d, uint32_t a, uint32_t b, uint3
       " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n"
       " add.u32 x, %1, 24;\n"
       " add.u32 y, %2, 384;\n"
-      " mov.b64 b, {y, %4};\n"
-      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n"
-      " add.u32 x, %1, 32;\n"
-      " add.u32 y, %2, 512;\n"
-      " mov.b64 b, {y, %4};\n"
-      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n"
-      " add.u32 x, %1, 40;\n"
-      " add.u32 y, %2, 640;\n"
-      " mov.b64 b, {y, %4};\n"
-      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n"
-      " add.u32 x, %1, 48;\n"
-      " add.u32 y, %2, 768;\n"
-      " mov.b64 b, {y, %4};\n"
-      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n"
-      " add.u32 x, %1, 56;\n"
-      " add.u32 y, %2, 896;\n"
       " mov.b64 b, {y, %4};\n"
       " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n"
       "}\n" ::"r"(d),
@@ -296,277 +311,392 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r) {
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  asm volatile("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
-  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  asm volatile("max.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
+}
+// A pair of fp32 registers: x c + b, and a sum.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm volatile("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, uint32_t &lo, uint32_t &hi) {
+  asm volatile("mov.b64 {%0, %1}, %2;\n" : "=r"(lo), "=r"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t c, uint64_t b) {
+  uint64_t r;
+  asm volatile("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(x), "l"(c), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm volatile("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm volatile("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t half2_of(uint32_t lo, uint32_t hi) {
+  uint32_t r;
+  asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
+  return r;
 }
 
 // ---------------------------------------------------------------------------- copies
-// Copy c brings K of pass c / 2 (even c) or its V (odd c) into stage c % kStages.
-__device__ __forceinline__ void load_role(const Maps &maps, const Work &w, Bars &sh, int lane) {
+// The CTA's copies are counted through all its blocks: copy number c goes to stage
+// c % kStages.  Pass i of a block takes K from the block's copy 2 i and V from 2 i + 1.
+__device__ __forceinline__ void load_role(const Maps &maps, const Cta &cta, Bars &sh, int lane) {
   bool ok = true;
-  int issued = 0;
-  if (lane == 0) {
-    for (int x = 0; x < 2; ++x)
-      if (w.on[x]) {
-        bar_expect(&sh.q[x], kTileBytes);
+  int c = 0, loads[2] = {0, 0};
+  Block w;
+  for (int k = 0; ok && block_of(cta, sh.list, k, &w); ++k) {
+    for (int i = 0; i < 2 * w.n && ok; ++i) {
+      const int st = c % kStages;
+      if (c >= kStages) ok = __all_sync(0xffffffffu, bar_wait(&sh.empty[st], (c / kStages - 1) & 1, &sh.abort));
+      if (!ok) break;
+      if (lane == 0) {
+        bar_expect(&sh.full[st], kTileBytes);
         for (int half = 0; half < 2; ++half)
-          tma_3d(w.sQ + x * kTileBytes + half * kHalfBytes, &maps.q, 64 * half, w.start + w.base[x], w.head0, &sh.q[x]);
+          tma_3d(cta.sKV + st * kTileBytes + half * kHalfBytes, i & 1 ? &maps.v : &maps.k, 64 * half,
+                 w.start + (w.n - 1 - i / 2) * kRows, w.kvh, &sh.full[st]);
       }
-  }
-  for (int c = 0; c < 2 * w.n && ok; ++c) {
-    const int st = c % kStages;
-    if (c >= kStages) ok = __all_sync(0xffffffffu, bar_wait(&sh.empty[st], (c / kStages - 1) & 1, &sh.abort));
-    if (ok && lane == 0) {
-      bar_expect(&sh.full[st], kTileBytes);
-      for (int half = 0; half < 2; ++half)
-        tma_3d(w.sKV + st * kTileBytes + half * kHalfBytes, c & 1 ? &maps.v : &maps.k, 64 * half,
-               w.start + (w.n - 1 - c / 2) * kRows, w.kvh, &sh.full[st]);
-    }
-    issued += ok;
-    if (c == min(2 * w.n, kStages) - 1 && w.tail < kRows) {
-      // the value rows behind the sequence, in copy 1: its first use waits for `zeroed`
-      ok = __all_sync(0xffffffffu, bar_wait(&sh.full[1], 0, &sh.abort));
-      unsigned char *v = w.tiles + (2 + 1) * kTileBytes;
-      for (int r = w.tail * 8 + lane; r < kRows * 8; r += 32)
-        for (int half = 0; half < 2; ++half)
-          *reinterpret_cast<uint4 *>(v + half * kHalfBytes + r * 16) = make_uint4(0u, 0u, 0u, 0u);
-      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-      __syncwarp();
-      if (lane == 0) bar_arrive(&sh.zeroed);
+      ++c;
+      if (i == 0) {  // Q behind the first K, which never waits for the block before
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (x && !w.nt1) break;
+          if (loads[x]) ok = __all_sync(0xffffffffu, bar_wait(&sh.q_free[x], (loads[x] - 1) & 1, &sh.abort));
+          if (!ok) break;
+          if (lane == 0) {
+            bar_expect(&sh.q[x], kTileBytes);
+            for (int half = 0; half < 2; ++half)
+              tma_3d(cta.sQ + x * kTileBytes + half * kHalfBytes, &maps.q, 64 * half, w.start + (x ? w.base1 : w.base0),
+                     w.head0, &sh.q[x]);
+          }
+          ++loads[x];
+        }
+      }
     }
   }
-  if (!ok && lane == 0) {  // the copies in flight land before the CTA ends
-    int never = 0;
-    for (int x = 0; x < 2 && !never; ++x)
-      if (w.on[x]) bar_wait(&sh.q[x], 0, &never);
-    for (int c = max(0, issued - kStages); c < issued && !never; ++c)
-      bar_wait(&sh.full[c % kStages], (c / kStages) & 1, &never);
-  }
+  // The CTA ends when nothing is under way any more: every copy has landed, and every
+  // arrival that the MMAs still owe has come.
+  int never = 0;
+  for (int x = 0; x < 2 && !never; ++x)
+    if (loads[x]) bar_wait(&sh.q[x], (loads[x] - 1) & 1, &never);
+  for (int j = max(0, c - kStages); j < c && !never; ++j) bar_wait(&sh.full[j % kStages], (j / kStages) & 1, &never);
+  for (int x = 0; x < 2 && ok; ++x)
+    if (loads[x]) ok = bar_wait(&sh.q_free[x], (loads[x] - 1) & 1, &sh.abort);
+  for (int j = max(0, c - kStages); j < c && ok; ++j) ok = bar_wait(&sh.empty[j % kStages], (j / kStages) & 1, &sh.abort);
+  __syncwarp();
+}
+
+// The rows of a value tile from `tail` on.
+__device__ __forceinline__ void zero_rows(unsigned char *v, int tail, int lane) {
+  for (int r = tail * 8 + lane; r < kRows * 8; r += 32)
+    for (int half = 0; half < 2; ++half)
+      *reinterpret_cast<uint4 *>(v + half * kHalfBytes + r * 16) = make_uint4(0u, 0u, 0u, 0u);
+  asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
   __syncwarp();
 }
 
 // -------------------------------------------------------------------------- products
-__device__ __forceinline__ void mma_role(const Work &w, Bars &sh) {
+// Of tile x.  Scores and output of one tile take turns in its warp; the other tile's warp
+// keeps the tensor cores busy meanwhile.
+__device__ __forceinline__ void mma_role(const Cta &cta, Bars &sh, int x, int lane) {
   const uint32_t one = elect_one();
-  bool ok = true;
-  const uint32_t q0 = desc_lo(w.sQ, 16), k0 = desc_lo(w.sKV, 16), v0 = desc_lo(w.sKV, kHalfBytes);
+  const uint32_t q0 = desc_lo(cta.sQ + x * kTileBytes, 16), k0 = desc_lo(cta.sKV, 16), v0 = desc_lo(cta.sKV, kHalfBytes);
+  const uint32_t tS = cta.tmem + x * kRows, tO = cta.tmem + 2 * kRows + x * kD;
   constexpr uint32_t kTile16 = kTileBytes >> 4;
   auto wait = [&](uint64_t *b, uint32_t parity) { return __all_sync(0xffffffffu, bar_wait(b, parity, &sh.abort)) != 0; };
-  auto qk = [&](int x, int st) {  // scores of tile x with the K tile in stage st
-    mma_qk(w.tmem + x * kRows, q0 + x * kTile16, k0 + st * kTile16, kIdescQK, 0, one);
+  auto landed = [&](int c) { return wait(&sh.full[c % kStages], (c / kStages) & 1); };
+  auto give = [&](int c) { tc_commit(&sh.empty[c % kStages], one); };
+  // Output of pass t of the tile with the V tile of copy c, keys 64 g .. 64 g + 63: the first half
+  // runs while the softmax works on the second.  The first pass of a block starts a new output,
+  // its probabilities coming after the softmax has read the last one.
+  auto pv = [&](int t, int c, int g, bool add) {
+    if (!wait(&sh.p[x][g], t & 1)) return false;
+    tc_fence_after();
+    mma_pv(tO, tS + 32 * g, v0 + (c % kStages) * kTile16 + 512 * g, kIdescPV, add, one);
+    tc_commit(&sh.o[x][g], one);
+    return true;
+  };
+  auto qk = [&](int c) {  // scores with the K tile of copy c
+    mma_qk(tS, q0, k0 + (c % kStages) * kTile16, kIdescQK, 0, one);
     tc_commit(&sh.s[x], one);
+    give(c);
   };
-  auto pv = [&](int x, int st, bool acc) {  // output of tile x with the V tile in stage st
-    mma_pv(w.tmem + 2 * kRows + x * kD, w.tmem + x * kRows, v0 + st * kTile16, kIdescPV, acc, one);
-    tc_commit(&sh.o[x], one);
-  };
-  // A stage is handed back only where a later copy waits for it: no arrival is left over
-  // when the CTA ends.
-  auto give = [&](int c, int st) {
-    if (c + kStages < 2 * w.n) tc_commit(&sh.empty[st], one);
-  };
-  const int nt0 = w.nt[0], nt1 = w.nt[1];
-  int done0 = 0, done1 = 0;  // P.V products of each tile
-  ok = wait(&sh.q[0], 0);
-  if (ok && nt1) ok = wait(&sh.q[1], 0);
-  ok = ok && wait(&sh.full[0], 0);
-  tc_fence_after();
-  if (ok) {
-    if (w.n <= nt0) qk(0, 0);
-    if (w.n <= nt1) qk(1, 0);
-    give(0, 0);
-    if (w.tail < kRows) ok = wait(&sh.zeroed, 0);
-  }
-  int sv = 1, sk = 2, cv = 1;       // stages of V of pass i and K of pass i + 1; copy of the former
-  uint32_t pv_par = 0, pk_par = 0;  // and their phases
-  for (int i = 0; i < w.n && ok; ++i) {
-    const int left = w.n - 1 - i;  // key tile of this pass
-    const bool more = left > 0;
-    ok = wait(&sh.full[sv], pv_par);
-    if (ok && left < nt0) {
-      ok = wait(&sh.p[0], done0 & 1);
-      if (!ok) break;
-      tc_fence_after();
-      pv(0, sv, done0 > 0);
-      ++done0;
+  int c = 0, t = 0, tiles = 0, zeroed = 0;  // copies, passes, Q tiles and zeroed value tiles before
+  Block w;
+  for (int k = 0; block_of(cta, sh.list, k, &w); ++k) {
+    const int nt = x ? w.nt1 : w.nt0;
+    for (int i = 0; i < 2 * (w.n - nt); ++i, ++c) {  // passes that are the other tile's alone
+      if (!landed(c)) return;
+      if (one) bar_arrive(&sh.empty[c % kStages]);
     }
-    if (ok && more) ok = wait(&sh.full[sk], pk_par);
-    if (!ok) break;
-    // the scores go where the probabilities were: MMAs run in the order of issue
-    if (more && left - 1 < nt0) qk(0, sk);
-    if (left < nt1) {
-      ok = wait(&sh.p[1], done1 & 1);
-      if (!ok) break;
-      tc_fence_after();
-      pv(1, sv, done1 > 0);
-      ++done1;
-    }
-    give(cv, sv);
-    if (more && left - 1 < nt1) qk(1, sk);
-    give(cv + 1, sk);
-    cv += 2;
-    sv += 2;
-    if (sv >= kStages) {
-      sv -= kStages;
-      pv_par ^= 1;
-    }
-    sk += 2;
-    if (sk >= kStages) {
-      sk -= kStages;
-      pk_par ^= 1;
+    if (nt == 0) continue;
+    if (!wait(&sh.q[x], tiles & 1) || !landed(c)) return;
+    ++tiles;
+    tc_fence_after();
+    qk(c);
+    for (int i = 0; i < nt; ++i, ++t, c += 2) {
+      const bool more = i + 1 < nt;
+      if (!more) tc_commit(&sh.q_free[x], one);
+      if (!landed(c + 1)) return;
+      if (i == 0 && nt == w.n && w.tail < kRows) {
+        // value rows behind the sequence: B's warp clears them for both tiles
+        const bool shared = w.nt0 == w.nt1;
+        if (x == 1 || !shared)
+          zero_rows(cta.tiles + (2 + (c + 1) % kStages) * kTileBytes, w.tail, lane);
+        else if (!wait(&sh.zeroed, zeroed & 1))
+          return;
+        if (x == 1 && shared && lane == 0) bar_arrive(&sh.zeroed);
+        zeroed += shared;
+      }
+      if (!pv(t, c + 1, 0, i > 0)) return;
+      if (more && !landed(c + 2)) return;
+      if (!pv(t, c + 1, 1, true)) return;
+      give(c + 1);
+      // the scores go where the probabilities were: MMAs run in the order of issue
+      if (more) qk(c + 2);
     }
   }
 }
 
 // --------------------------------------------------------------------------- softmax
-__device__ __forceinline__ void softmax_role(const PackedAttentionArgs &a, const Work &w, Bars &sh, int x, int warp,
+// Marks 32 registers as written here: what reads them stays behind the wait before.
+__device__ __forceinline__ void landed32(uint32_t *r) {
+#pragma unroll
+  for (int k = 0; k < 32; k += 8)
+    asm volatile(""
+                 : "+r"(r[k]), "+r"(r[k + 1]), "+r"(r[k + 2]), "+r"(r[k + 3]), "+r"(r[k + 4]), "+r"(r[k + 5]),
+                   "+r"(r[k + 6]), "+r"(r[k + 7]));
+}
+
+__device__ __forceinline__ float max64(const uint32_t *s) {
+  float mx[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) mx[j] = fmaxf(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
+#pragma unroll
+  for (int k = 8; k < 64; k += 8)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], __uint_as_float(s[k + 2 * j]), __uint_as_float(s[k + 2 * j + 1]));
+  return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+}
+
+// Probabilities 2^(c0 s + b) of 64 scores, as fp16 pairs in p, added to the two sums in l;
+// returns the largest exponent.  s is used up.  Written in batches of 8, the sums and
+// conversions of a batch behind the exponentials of the next one, so that the exponential
+// unit (8 lanes a cycle, the bound of this function: 256 cycles) is not waited for.
+__device__ __forceinline__ float exp64(uint32_t *s, uint32_t *p, uint64_t c2, uint64_t b2, uint64_t *l) {
+  float mx[4];
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    const uint64_t e = fma2(pair(s[2 * k], s[2 * k + 1]), c2, b2);
+    unpair(e, s[2 * k], s[2 * k + 1]);
+  }
+  auto finish = [&](int j) {  // sums and conversions of batch j
+#pragma unroll
+    for (int i = 4 * j; i < 4 * j + 4; ++i) {
+      l[i & 1] = add2(l[i & 1], pair(s[2 * i], s[2 * i + 1]));
+      p[i] = half2_of(s[2 * i], s[2 * i + 1]);
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float u = __uint_as_float(s[8 * j + 2 * i]), v = __uint_as_float(s[8 * j + 2 * i + 1]);
+      mx[i] = j ? max3(mx[i], u, v) : fmaxf(u, v);
+    }
+#pragma unroll
+    for (int i = 8 * j; i < 8 * j + 8; ++i) s[i] = __float_as_uint(ex2(__uint_as_float(s[i])));
+    if (j) finish(j - 1);
+  }
+  finish(7);
+  return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+}
+
+__device__ __forceinline__ void softmax_role(const PackedAttentionArgs &a, const Cta &cta, Bars &sh, int x, int warp,
                                              int lane) {
   const int r = 32 * warp + lane;  // row of tile x
   const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-  const uint32_t tS = w.tmem + x * kRows + lanes, tO = w.tmem + 2 * kRows + x * kD + lanes;
-  const int base = x ? w.base[1] : w.base[0], nt = x ? w.nt[1] : w.nt[0];
-  const int token = base + r % w.tpt;
+  const uint32_t tS = cta.tmem + x * kRows + lanes, tO = cta.tmem + 2 * kRows + x * kD + lanes;
   const float c0 = a.softmax_scale * kLog2eP;
-  float m = -INFINITY, l = 0.f;
-  bool ok = true;
-  for (int t = 0; t < nt; ++t) {
-    ok = __all_sync(0xffffffffu, bar_wait(&sh.s[x], t & 1, &sh.abort));
-    if (!ok) break;
-    tc_fence_after();
-    uint32_t s[kRows];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) tmem_ld32(tS + 32 * k, s + 32 * k);
-    tc_wait_ld();
-    if (t == 0) {  // the tile on the diagonal
-      const int last = token - (nt - 1) * kRows;  // the row's own key in it
-#pragma unroll
-      for (int k = 0; k < kRows; ++k)
-        if (k > last) s[k] = 0xff800000u;
-    }
-    float mx0 = __uint_as_float(s[0]), mx1 = __uint_as_float(s[1]);
-#pragma unroll
-    for (int k = 2; k + 3 < kRows; k += 4) {
-      mx0 = max3(mx0, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-      mx1 = max3(mx1, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
-    }
-    mx0 = max3(mx0, __uint_as_float(s[kRows - 2]), __uint_as_float(s[kRows - 1]));
-    const float mx = fmaxf(mx0, mx1);
-    if (t == 0) {
-      m = mx;
-    } else if (__any_sync(0xffffffffu, (mx - m) * c0 > kLag)) {
-      const float mn = fmaxf(m, mx);
-      const float al = ex2((m - mn) * c0);
-      m = mn;
-      l *= al;
-      ok = __all_sync(0xffffffffu, bar_wait(&sh.o[x], (t - 1) & 1, &sh.abort));
-      if (!ok) break;
-      tc_fence_after();
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t o[32];
-        tmem_ld32(tO + 32 * k, o);
-        tc_wait_ld();
-#pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * al);
-        tmem_st32(tO + 32 * k, o);
-      }
-    }
-    const float b = kShift - m * c0;
-    const float2 c2 = make_float2(c0, c0), b2 = make_float2(b, b);
-    float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-#pragma unroll
-    for (int k = 0; k < kRows / 2; ++k) {
-      const float2 e = __ffma2_rn(make_float2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), c2, b2);
-      const float2 p = make_float2(ex2(e.x), ex2(e.y));
-      if (k & 1)
-        sum1 = __fadd2_rn(sum1, p);
-      else
-        sum0 = __fadd2_rn(sum0, p);
-      s[k] = h22u(__floats2half2_rn(p.x, p.y));
-    }
-    sum0 = __fadd2_rn(sum0, sum1);
-    l += sum0.x + sum0.y;
-    tmem_st32(tS, s);
-    tmem_st32(tS + 32, s + 32);
+  const uint64_t c2 = pair(__float_as_uint(c0), __float_as_uint(c0));
+  // whole 32-byte sectors where the output's rows allow it
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.out.p) | (uintptr_t)(a.out.ts * 2) | (uintptr_t)(a.out.hs * 2)) & 31) == 0;
+  auto wait = [&](uint64_t *b, uint32_t parity) { return __all_sync(0xffffffffu, bar_wait(b, parity, &sh.abort)) != 0; };
+  // the probabilities of keys 64 g .. 64 g + 63 go over the first half of the scores, read by then
+  auto put = [&](int g, const uint32_t *p) {
+    tmem_st32(tS + 32 * g, p);
     tc_wait_st();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) bar_arrive(&sh.p[x]);
-  }
-  if (ok) ok = __all_sync(0xffffffffu, bar_wait(&sh.o[x], (nt - 1) & 1, &sh.abort));
-  tc_fence_after();
-  // ---- the tile's rows, through the shared memory of its Q tile (16-byte chunk c of row r
-  // at chunk c ^ (r % 8)), then written row by row
-  const float inv = ok ? 1.f / l : __int_as_float(0x7fc00000);
-  unsigned char *so = w.tiles + x * kTileBytes;
+    if (lane == 0) bar_arrive(&sh.p[x][g]);
+  };
+  bool ok = true;
+  int t0 = 0;  // passes of this tile in the blocks before
+  Block w;
+  for (int k = 0; block_of(cta, sh.list, k, &w); ++k) {
+    const int base = x ? w.base1 : w.base0, nt = x ? w.nt1 : w.nt0;
+    if (nt == 0) continue;
+    const int token = base + r % cta.tpt;
+    float m = 0.f;           // the reference maximum
+    uint64_t l[2] = {0, 0};  // the sum, in four parts
+    uint64_t b2 = 0;         // the exponents' offset with this maximum, twice
+    auto refer = [&](float mx) {
+      m = mx;
+      const uint32_t b = __float_as_uint(kShift - m * c0);
+      b2 = pair(b, b);
+    };
+    uint32_t s[kRows], p[32];
+    ok = ok && wait(&sh.s[x], t0 & 1);
+    if (ok) {  // the tile on the diagonal
+      tc_fence_after();
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    uint32_t o[32];
-    tmem_ld32(tO + 32 * k, o);
-    tc_wait_ld();
+      for (int j = 0; j < 4; ++j) tmem_ld32(tS + 32 * j, s + 32 * j);
+      tc_wait_ld();
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t h[4];
+      for (int j = 0; j < 4; ++j) landed32(s + 32 * j);
+      const int last = token - (nt - 1) * kRows;  // the row's own key in it
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        h[j] = h22u(__floats2half2_rn(__uint_as_float(o[8 * c + 2 * j]) * inv,
-                                      __uint_as_float(o[8 * c + 2 * j + 1]) * inv));
-      *reinterpret_cast<uint4 *>(so + r * 256 + ((4 * k + c) ^ (r & 7)) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+      for (int j = 0; j < kRows; ++j)
+        if (j > last) s[j] = 0xff800000u;
+      refer(fmaxf(max64(s), max64(s + 64)));
+      exp64(s, p, c2, b2, l);
+      put(0, p);
+      exp64(s + 64, p, c2, b2, l);
+      put(1, p);
     }
-  }
-  __syncwarp();
-  for (int it = 0; it < 16; ++it) {
-    const int rr = 32 * warp + 2 * it + (lane >> 4), c = lane & 15;
-    const int tok = base + rr % w.tpt;
-    if (tok < w.len) {
-      uint16_t *dst = a.out.p + (int64_t)(w.start + tok) * a.out.ts + (int64_t)(w.head0 + rr / w.tpt) * a.out.hs + 8 * c;
-      *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(so + rr * 256 + (c ^ (rr & 7)) * 16);
+    for (int t = t0 + 1; t < t0 + nt && ok; ++t) {
+      ok = wait(&sh.s[x], t & 1);
+      if (!ok) break;
+      tc_fence_after();
+      tmem_ld32(tS, s);
+      tmem_ld32(tS + 32, s + 32);
+      tc_wait_ld();
+      landed32(s);
+      landed32(s + 32);
+      tmem_ld32(tS + 64, s + 64);
+      tmem_ld32(tS + 96, s + 96);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        if (g == 1) {
+          tc_wait_ld();
+          landed32(s + 64);
+          landed32(s + 96);
+        }
+        // with the maximum of before, which nearly always still serves: whether it does is
+        // found beside the exponentials instead of before them
+        const uint64_t l0 = l[0], l1 = l[1];
+        const float over = exp64(s + 64 * g, p, c2, b2, l);
+        if (__any_sync(0xffffffffu, over > kShift + kLag)) {
+          tmem_ld32(tS + 64 * g, s + 64 * g);
+          tmem_ld32(tS + 64 * g + 32, s + 64 * g + 32);
+          tc_wait_ld();
+          landed32(s + 64 * g);
+          landed32(s + 64 * g + 32);
+          const float mn = fmaxf(m, max64(s + 64 * g));
+          const float al = ex2((m - mn) * c0);
+          refer(mn);
+          const uint64_t al2 = pair(__float_as_uint(al), __float_as_uint(al));
+          l[0] = mul2(l0, al2);
+          l[1] = mul2(l1, al2);
+          ok = wait(&sh.o[x][g ^ 1], (t - 1 + g) & 1);  // the last product into the output
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32 * j, o);
+            tc_wait_ld();
+            landed32(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+            tmem_st32(tO + 32 * j, o);
+          }
+          exp64(s + 64 * g, p, c2, b2, l);
+        }
+        put(g, p);
+      }
     }
+    t0 += nt;
+    ok = ok && wait(&sh.o[x][0], (t0 - 1) & 1) && wait(&sh.o[x][1], (t0 - 1) & 1);
+    tc_fence_after();
+    // ---- the tile's rows
+    uint32_t l_lo, l_hi;
+    unpair(add2(l[0], l[1]), l_lo, l_hi);
+    const float inv = ok ? 1.f / (__uint_as_float(l_lo) + __uint_as_float(l_hi)) : __int_as_float(0x7fc00000);
+    uint16_t *dst = a.out.p + (int64_t)(w.start + token) * a.out.ts + (int64_t)(w.head0 + r / cta.tpt) * a.out.hs;
+    const bool mine = token < w.len;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t o[32], h[16];
+      tmem_ld32(tO + 32 * j, o);
+      tc_wait_ld();
+      landed32(o);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        h[i] = half2_of(__float_as_uint(__uint_as_float(o[2 * i]) * inv), __float_as_uint(__uint_as_float(o[2 * i + 1]) * inv));
+      if (mine) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint16_t *d = dst + 32 * j + 16 * i;
+          const uint32_t *v = h + 8 * i;
+          if (wide) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(d), "r"(v[0]), "r"(v[1]),
+                         "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                         : "memory");
+          } else {
+            *reinterpret_cast<uint4 *>(d) = make_uint4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<uint4 *>(d + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+          }
+        }
+      }
+    }
+    tc_fence_before();  // the output is read: the next block's probabilities say so
   }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
     packed_attention_kernel(const __grid_constant__ PackedAttentionArgs a, const __grid_constant__ Maps maps, int pack) {
   extern __shared__ unsigned char raw[];
-  Work w;
+  Cta cta;
   // tiles start at a multiple of the swizzle's 1024-byte pattern
-  w.tiles = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  Bars &sh = *reinterpret_cast<Bars *>(w.tiles + (2 + kStages) * kTileBytes);
-  w.sQ = smem_u32(w.tiles);
-  w.sKV = w.sQ + 2 * kTileBytes;
+  cta.tiles = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  Bars &sh = *reinterpret_cast<Bars *>(cta.tiles + (2 + kStages) * kTileBytes);
+  cta.sQ = smem_u32(cta.tiles);
+  cta.sKV = cta.sQ + 2 * kTileBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  w.tpt = kRows / pack;
-  const unsigned hgroups = (unsigned)(a.Hq / pack);  // head groups that share a tile
-  w.head0 = (int)(blockIdx.x % hgroups) * pack;
-  w.kvh = w.head0 / (a.Hq / a.Hkv);
+  cta.tpt = kRows / pack;
+  cta.pack = pack;
+  cta.heads_per_kv = a.Hq / a.Hkv;
+  cta.hgroups = (unsigned)(a.Hq / pack);
 
-  if (warp == 0) {
-    PackedBlock blk = {};
-    const bool found = packed_block(a.cu, a.n_seqs, a.T, 2 * w.tpt, blockIdx.x / hgroups, &blk);
-    if (lane == 0) {
-      sh.found = found;
-      sh.blk = blk;
-      sh.abort = 0;
-    }
-  }
   if (warp == kMmaWarp) {
     if (lane == 0) {
       for (int x = 0; x < 2; ++x) {
         bar_init(&sh.q[x], 1);
+        bar_init(&sh.q_free[x], 1);
         bar_init(&sh.s[x], 1);
-        bar_init(&sh.p[x], 4);
-        bar_init(&sh.o[x], 1);
+        for (int g = 0; g < 2; ++g) {
+          bar_init(&sh.p[x][g], 4);
+          bar_init(&sh.o[x][g], 1);
+        }
       }
       for (int i = 0; i < kStages; ++i) {
         bar_init(&sh.full[i], 1);
-        bar_init(&sh.empty[i], 1);
+        bar_init(&sh.empty[i], 2);
       }
       bar_init(&sh.zeroed, 1);
+      sh.abort = 0;
       asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     __syncwarp();
@@ -575,39 +705,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
   }
+  sh.list.build(a.cu, a.n_seqs, a.T, 2 * cta.tpt);  // the CTA's threads together
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  w.tmem = sh.tmem;
-  if (sh.found) {
-    w.start = sh.blk.start;
-    w.len = sh.blk.len;
-    w.base[0] = sh.blk.level * 2 * w.tpt;
-    w.base[1] = w.base[0] + w.tpt;
-    w.on[0] = true;
-    w.on[1] = w.base[1] < w.len;
-    w.nt[0] = w.base[0] / kRows + 1;
-    w.nt[1] = w.on[1] ? w.base[1] / kRows + 1 : 0;
-    w.n = max(w.nt[0], w.nt[1]);
-    w.tail = w.len - (w.n - 1) * kRows;
-    if (warp >= kMmaWarp) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
-      if (warp == kLoadWarp) {
-        load_role(maps, w, sh, lane);
-      } else if (warp == kMmaWarp) {
-        mma_role(w, sh);
-      }
-    } else {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
-      const int x = warp >> 2;
-      if (x == 0 || w.on[1]) softmax_role(a, w, sh, x, warp & 3, lane);
-    }
+  cta.tmem = sh.tmem;
+  cta.items = (int64_t)sh.list.total * cta.hgroups;
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+    if (warp == kLoadWarp)
+      load_role(maps, cta, sh, lane);
+    else if (warp < kLoadWarp)
+      mma_role(cta, sh, warp - kMmaWarp, lane);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
+    softmax_role(a, cta, sh, warp >> 2, warp & 3, lane);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == kMmaWarp)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(w.tmem), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(cta.tmem), "r"(kTmemCols) : "memory");
 }
 
 typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -647,31 +765,36 @@ int pack_of(const PackedAttentionArgs &a) {
   return p;
 }
 
-int64_t grid_of(const PackedAttentionArgs &a) {
+// Most blocks there can be: what the lengths allow.
+int64_t blocks_of(const PackedAttentionArgs &a) {
   const int pack = pack_of(a);
   return ((int64_t)a.T / (2 * kRows / pack) + a.n_seqs) * (a.Hq / pack);
 }
 
-// Once per device: the shared memory's limit, and that the kernel has the registers that the
-// warpgroups' split of them rests on.
-cudaError_t prepare_kernel() {
-  static std::atomic<uint64_t> ready{0};
+// SMs of the current device.  Once per device: the shared memory's limit, and that the kernel has
+// the registers that the warpgroups' split of them rests on.
+cudaError_t prepare_kernel(int *sms) {
+  static std::atomic<int> known[64];  // SMs + 1 of a device that is ready, else 0
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (ready.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const int n = dev < 64 ? known[dev].load(std::memory_order_acquire) : 0;
+  if (n) {
+    *sms = n - 1;
+    return cudaSuccess;
+  }
   cudaFuncAttributes f;
   if ((e = cudaFuncGetAttributes(&f, packed_attention_kernel)) != cudaSuccess) return e;
   if (f.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
   e = cudaFuncSetAttribute(packed_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && dev < 64) known[dev].store(*sms + 1, std::memory_order_release);
   return e;
 }
 
 }  // namespace
 
-bool packed_attention_fits(const PackedAttentionArgs &a) { return grid_of(a) <= 0x7fffffff; }
+bool packed_attention_fits(const PackedAttentionArgs &a) { return blocks_of(a) <= 0x7fffffff; }
 
 cudaError_t launch_packed_attention(const PackedAttentionArgs &a, cudaStream_t st) {
   const int pack = pack_of(a);
@@ -679,9 +802,10 @@ cudaError_t launch_packed_attention(const PackedAttentionArgs &a, cudaStream_t s
   if (!encode(&maps.q, a.q, a.T, a.Hq, kRows / pack, pack) || !encode(&maps.k, a.k, a.T, a.Hkv, kRows, 1) ||
       !encode(&maps.v, a.v, a.T, a.Hkv, kRows, 1))
     return cudaErrorInvalidValue;
-  cudaError_t e = prepare_kernel();
+  int sms = 0;
+  cudaError_t e = prepare_kernel(&sms);
   if (e != cudaSuccess) return e;
-  packed_attention_kernel<<<(unsigned)grid_of(a), kThreads, kSmem, st>>>(a, maps, pack);
+  packed_attention_kernel<<<(unsigned)std::min<int64_t>(blocks_of(a), sms), kThreads, kSmem, st>>>(a, maps, pack);
   return cudaGetLastError();
 }
 
