@@ -22,7 +22,8 @@
 //                   shared memory) and O += P V (P in tensor memory); one tile's softmax
 //                   runs under the other's MMAs.
 //   warp 10         one lane issues the tensor-map copies: Q, and K and V tiles through a
-//                   ring of stages.  (Warp 11 is idle: registers go by four warps.)
+//                   ring of stages.
+//   warp 11         finds the CTA's next block, one ahead.
 // Tensor memory: S/P of A and B (128 columns each), O of A and B (128 each): all 512.
 //
 // The maximum that the probabilities are relative to may lag behind the true one by 2^8:
@@ -64,9 +65,21 @@ constexpr int kStages = 4;                  // K and V tiles in flight
 constexpr int kMaxPack = 16;
 constexpr float kLag = 8.f;                 // log2 by which the reference maximum may lag
 constexpr float kShift = 7.f;               // log2 of the probabilities' scale
+constexpr float kFar = 1 << 16;             // |log2 score| from which an offset in fp32 (2^-8 there) is not enough
 constexpr float kLog2eP = 1.4426950408889634f;
 constexpr int kPolls = 1 << 22;             // of a wait, each suspended by the hardware for a while
 constexpr uint32_t kTmemCols = 512;
+
+// One block of work.
+struct __align__(16) Block {
+  int start, len;         // the sequence
+  int head0, kvh;
+  int base0, base1;       // first token of A, of B
+  int nt0, nt1;           // key tiles of each, the last one on the diagonal (B: 0 when it has no row)
+  int n;                  // passes: pass i works on key tile n - 1 - i
+  int tail;               // rows of the last key tile inside the sequence (more than a tile: all)
+  int there;              // 0: no block, and none after it
+};
 
 struct __align__(16) Bars {
   uint64_t q[2];            // Q tile landed
@@ -77,6 +90,9 @@ struct __align__(16) Bars {
   uint64_t p[2][2];         // the probabilities of its first, its second 64 keys written
   uint64_t o[2][2];         // their P.V done
   uint64_t zeroed;          // value rows behind the sequence overwritten, for tile A
+  uint64_t block[2];        // block k written to slot k % 2
+  uint64_t block_read[2];   // by every warp that works on it
+  Block slot[2];
   uint32_t tmem;
   int abort;
   PackedList list;
@@ -98,36 +114,6 @@ struct Cta {
   int heads_per_kv, pack;
   int64_t items;          // blocks of all sequences and head groups
 };
-
-// One block of work.
-struct Block {
-  int start, len;         // the sequence
-  int head0, kvh;
-  int base0, base1;       // first token of A, of B
-  int nt0, nt1;           // key tiles of each, the last one on the diagonal (B: 0 when it has no row)
-  int n;                  // passes: pass i works on key tile n - 1 - i
-  int tail;               // rows of the last key tile inside the sequence (more than a tile: all)
-};
-
-// Block k of this CTA: the list is dealt out back and forth, so that the first CTAs do not
-// get the longer block of every round.
-__device__ __forceinline__ bool block_of(const Cta &c, const PackedList &list, int k, Block *w) {
-  const int64_t G = gridDim.x, at = k * G + ((k & 1) ? G - 1 - blockIdx.x : blockIdx.x);
-  if (at >= c.items) return false;
-  const unsigned item = (unsigned)(at / c.hgroups), hg = (unsigned)(at - (int64_t)item * c.hgroups);
-  const PackedBlock b = list.find(item);
-  w->start = b.start;
-  w->len = b.len;
-  w->head0 = (int)hg * c.pack;
-  w->kvh = w->head0 / c.heads_per_kv;
-  w->base0 = b.level * 2 * c.tpt;
-  w->base1 = w->base0 + c.tpt;
-  w->nt0 = w->base0 / kRows + 1;
-  w->nt1 = w->base1 < w->len ? w->base1 / kRows + 1 : 0;
-  w->n = max(w->nt0, w->nt1);
-  w->tail = w->len - (w->n - 1) * kRows;
-  return true;
-}
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -349,6 +335,50 @@ __device__ __forceinline__ uint32_t half2_of(uint32_t lo, uint32_t hi) {
   return r;
 }
 
+// ---------------------------------------------------------------------------- blocks
+constexpr int kReaders = 11;  // warps that work on a block
+
+// Block k of this CTA into slot k % 2, for the warps that work on it.  The list is dealt out
+// back and forth, so that the first CTAs do not get the longer block of every round.
+__device__ __forceinline__ void block_role(const Cta &c, Bars &sh, int lane) {
+  const int64_t G = gridDim.x;
+  for (int k = 0;; ++k) {
+    const int64_t at = k * G + ((k & 1) ? G - 1 - blockIdx.x : blockIdx.x);
+    Block w = {};
+    w.there = at < c.items;
+    if (w.there) {
+      const unsigned item = (unsigned)at / c.hgroups, hg = (unsigned)at - item * c.hgroups;
+      const PackedBlock b = sh.list.find(item);
+      w.start = b.start;
+      w.len = b.len;
+      w.head0 = (int)hg * c.pack;
+      w.kvh = w.head0 / c.heads_per_kv;
+      w.base0 = b.level * 2 * c.tpt;
+      w.base1 = w.base0 + c.tpt;
+      w.nt0 = w.base0 / kRows + 1;
+      w.nt1 = w.base1 < w.len ? w.base1 / kRows + 1 : 0;
+      w.n = max(w.nt0, w.nt1);
+      w.tail = w.len - (w.n - 1) * kRows;
+    }
+    if (k >= 2 && !__all_sync(0xffffffffu, bar_wait(&sh.block_read[k & 1], (k / 2 - 1) & 1, &sh.abort))) return;
+    if (lane == 0) {
+      sh.slot[k & 1] = w;
+      bar_arrive(&sh.block[k & 1]);
+    }
+    __syncwarp();
+    if (!w.there) return;
+  }
+}
+
+// A warp's next block; false after the last one (or an abort).
+__device__ __forceinline__ bool next_block(Bars &sh, int k, int lane, Block *w) {
+  if (!__all_sync(0xffffffffu, bar_wait(&sh.block[k & 1], (k >> 1) & 1, &sh.abort))) return false;
+  *w = sh.slot[k & 1];
+  __syncwarp();
+  if (lane == 0) bar_arrive(&sh.block_read[k & 1]);
+  return w->there != 0;
+}
+
 // ---------------------------------------------------------------------------- copies
 // The CTA's copies are counted through all its blocks: copy number c goes to stage
 // c % kStages.  Pass i of a block takes K from the block's copy 2 i and V from 2 i + 1.
@@ -356,7 +386,7 @@ __device__ __forceinline__ void load_role(const Maps &maps, const Cta &cta, Bars
   bool ok = true;
   int c = 0, loads[2] = {0, 0};
   Block w;
-  for (int k = 0; ok && block_of(cta, sh.list, k, &w); ++k) {
+  for (int k = 0; ok && next_block(sh, k, lane, &w); ++k) {
     for (int i = 0; i < 2 * w.n && ok; ++i) {
       const int st = c % kStages;
       if (c >= kStages) ok = __all_sync(0xffffffffu, bar_wait(&sh.empty[st], (c / kStages - 1) & 1, &sh.abort));
@@ -434,7 +464,7 @@ __device__ __forceinline__ void mma_role(const Cta &cta, Bars &sh, int x, int la
   };
   int c = 0, t = 0, tiles = 0, zeroed = 0;  // copies, passes, Q tiles and zeroed value tiles before
   Block w;
-  for (int k = 0; block_of(cta, sh.list, k, &w); ++k) {
+  for (int k = 0; next_block(sh, k, lane, &w); ++k) {
     const int nt = x ? w.nt1 : w.nt0;
     for (int i = 0; i < 2 * (w.n - nt); ++i, ++c) {  // passes that are the other tile's alone
       if (!landed(c)) return;
@@ -490,14 +520,12 @@ __device__ __forceinline__ float max64(const uint32_t *s) {
   return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
 }
 
-// Probabilities 2^(c0 s + b) of 64 scores, as fp16 pairs in p, added to the two sums in l;
-// returns the largest exponent.  s is used up.  Written in batches of 8, the sums and
-// conversions of a batch behind the exponentials of the next one, so that the exponential
-// unit (8 lanes a cycle, the bound of this function: 256 cycles) is not waited for.
-__device__ __forceinline__ float exp64(uint32_t *s, uint32_t *p, uint64_t c2, uint64_t b2, uint64_t *l) {
-  float mx[4];
+// Probabilities 2^(c0 s + b) of 32 scores, as fp16 pairs in p, added to the two sums in l;
+// the largest exponent goes into mx.  s is used up.  In batches of 8, the sums and
+// conversions of a batch behind the exponentials of the next one.
+__device__ __forceinline__ void exp32(uint32_t *s, uint32_t *p, uint64_t c2, uint64_t b2, uint64_t *l, float *mx) {
 #pragma unroll
-  for (int k = 0; k < 32; ++k) {
+  for (int k = 0; k < 16; ++k) {
     const uint64_t e = fma2(pair(s[2 * k], s[2 * k + 1]), c2, b2);
     unpair(e, s[2 * k], s[2 * k + 1]);
   }
@@ -509,18 +537,15 @@ __device__ __forceinline__ float exp64(uint32_t *s, uint32_t *p, uint64_t c2, ui
     }
   };
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 4; ++j) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float u = __uint_as_float(s[8 * j + 2 * i]), v = __uint_as_float(s[8 * j + 2 * i + 1]);
-      mx[i] = j ? max3(mx[i], u, v) : fmaxf(u, v);
-    }
+    for (int i = 0; i < 4; ++i)
+      mx[i] = max3(mx[i], __uint_as_float(s[8 * j + 2 * i]), __uint_as_float(s[8 * j + 2 * i + 1]));
 #pragma unroll
     for (int i = 8 * j; i < 8 * j + 8; ++i) s[i] = __float_as_uint(ex2(__uint_as_float(s[i])));
     if (j) finish(j - 1);
   }
-  finish(7);
-  return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+  finish(3);
 }
 
 __device__ __forceinline__ void softmax_role(const PackedAttentionArgs &a, const Cta &cta, Bars &sh, int x, int warp,
@@ -544,88 +569,86 @@ __device__ __forceinline__ void softmax_role(const PackedAttentionArgs &a, const
   bool ok = true;
   int t0 = 0;  // passes of this tile in the blocks before
   Block w;
-  for (int k = 0; block_of(cta, sh.list, k, &w); ++k) {
+  for (int k = 0; next_block(sh, k, lane, &w); ++k) {
     const int base = x ? w.base1 : w.base0, nt = x ? w.nt1 : w.nt0;
     if (nt == 0) continue;
     const int token = base + r % cta.tpt;
     float m = 0.f;           // the reference maximum
     uint64_t l[2] = {0, 0};  // the sum, in four parts
     uint64_t b2 = 0;         // the exponents' offset with this maximum, twice
+    // Far from zero the offset's rounding would count: there the maximum is subtracted first.
+    bool far = false;
     auto refer = [&](float mx) {
       m = mx;
-      const uint32_t b = __float_as_uint(kShift - m * c0);
+      far = __any_sync(0xffffffffu, fabsf(m * c0) > kFar);
+      const uint32_t b = __float_as_uint(far ? kShift : kShift - m * c0);
       b2 = pair(b, b);
     };
-    uint32_t s[kRows], p[32];
-    ok = ok && wait(&sh.s[x], t0 & 1);
-    if (ok) {  // the tile on the diagonal
-      tc_fence_after();
-#pragma unroll
-      for (int j = 0; j < 4; ++j) tmem_ld32(tS + 32 * j, s + 32 * j);
-      tc_wait_ld();
-#pragma unroll
-      for (int j = 0; j < 4; ++j) landed32(s + 32 * j);
-      const int last = token - (nt - 1) * kRows;  // the row's own key in it
-#pragma unroll
-      for (int j = 0; j < kRows; ++j)
-        if (j > last) s[j] = 0xff800000u;
-      refer(fmaxf(max64(s), max64(s + 64)));
-      exp64(s, p, c2, b2, l);
-      put(0, p);
-      exp64(s + 64, p, c2, b2, l);
-      put(1, p);
-    }
-    for (int t = t0 + 1; t < t0 + nt && ok; ++t) {
-      ok = wait(&sh.s[x], t & 1);
-      if (!ok) break;
-      tc_fence_after();
-      tmem_ld32(tS, s);
-      tmem_ld32(tS + 32, s + 32);
-      tc_wait_ld();
-      landed32(s);
-      landed32(s + 32);
-      tmem_ld32(tS + 64, s + 64);
-      tmem_ld32(tS + 96, s + 96);
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        if (g == 1) {
-          tc_wait_ld();
-          landed32(s + 64);
-          landed32(s + 96);
-        }
-        // with the maximum of before, which nearly always still serves: whether it does is
-        // found beside the exponentials instead of before them
-        const uint64_t l0 = l[0], l1 = l[1];
-        const float over = exp64(s + 64 * g, p, c2, b2, l);
-        if (__any_sync(0xffffffffu, over > kShift + kLag)) {
-          tmem_ld32(tS + 64 * g, s + 64 * g);
-          tmem_ld32(tS + 64 * g + 32, s + 64 * g + 32);
-          tc_wait_ld();
-          landed32(s + 64 * g);
-          landed32(s + 64 * g + 32);
-          const float mn = fmaxf(m, max64(s + 64 * g));
-          const float al = ex2((m - mn) * c0);
-          refer(mn);
-          const uint64_t al2 = pair(__float_as_uint(al), __float_as_uint(al));
-          l[0] = mul2(l0, al2);
-          l[1] = mul2(l1, al2);
-          ok = wait(&sh.o[x][g ^ 1], (t - 1 + g) & 1);  // the last product into the output
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t o[32];
-            tmem_ld32(tO + 32 * j, o);
-            tc_wait_ld();
-            landed32(o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-            tmem_st32(tO + 32 * j, o);
-          }
-          exp64(s + 64 * g, p, c2, b2, l);
-        }
-        put(g, p);
+    const int last = token - (nt - 1) * kRows;  // the row's own key in the tile on the diagonal
+    // 64 keys at a time, one body for all of them: code that is read once a block costs more
+    // than it runs
+    for (int q = 2 * t0; q < 2 * (t0 + nt) && ok; ++q) {
+      const int g = q & 1, t = q >> 1;
+      if (g == 0) {
+        ok = wait(&sh.s[x], t & 1);
+        if (!ok) break;
+        tc_fence_after();
       }
+      const bool diagonal = t == t0;
+      bool fresh = q == 2 * t0;  // the maximum has to be found before the exponentials
+      uint32_t p[32];
+      for (;;) {
+        uint32_t s[64];
+        tmem_ld32(tS + 64 * g, s);
+        tmem_ld32(tS + 64 * g + 32, s + 32);
+        tc_wait_ld();
+        landed32(s);
+        landed32(s + 32);
+        if (diagonal) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j)
+            if (j + 64 * g > last) s[j] = 0xff800000u;
+        }
+        if (fresh) {
+          float mn = max64(s);
+          if (q != 2 * t0) {
+            mn = fmaxf(m, mn);
+            const float al = ex2((m - mn) * c0);
+            const uint64_t al2 = pair(__float_as_uint(al), __float_as_uint(al));
+            l[0] = mul2(l[0], al2);
+            l[1] = mul2(l[1], al2);
+            ok = wait(&sh.o[x][g ^ 1], (t - 1 + g) & 1);  // the last product into the output
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+              uint32_t o[32];
+              tmem_ld32(tO + 32 * j, o);
+              tc_wait_ld();
+              landed32(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+              tmem_st32(tO + 32 * j, o);
+            }
+          }
+          refer(mn);
+        }
+        if (far) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) - m);
+        }
+        // With the maximum of before, which nearly always still serves: whether it does is
+        // found beside the exponentials instead of before them.
+        const uint64_t l0 = l[0], l1 = l[1];
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        exp32(s, p, c2, b2, l, mx);
+        exp32(s + 32, p + 16, c2, b2, l, mx);
+        if (fresh || !__any_sync(0xffffffffu, fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) > kShift + kLag)) break;
+        l[0] = l0;
+        l[1] = l1;
+        fresh = true;
+      }
+      if (ok) put(g, p);
     }
     t0 += nt;
     ok = ok && wait(&sh.o[x][0], (t0 - 1) & 1) && wait(&sh.o[x][1], (t0 - 1) & 1);
@@ -636,7 +659,7 @@ __device__ __forceinline__ void softmax_role(const PackedAttentionArgs &a, const
     const float inv = ok ? 1.f / (__uint_as_float(l_lo) + __uint_as_float(l_hi)) : __int_as_float(0x7fc00000);
     uint16_t *dst = a.out.p + (int64_t)(w.start + token) * a.out.ts + (int64_t)(w.head0 + r / cta.tpt) * a.out.hs;
     const bool mine = token < w.len;
-#pragma unroll
+#pragma unroll 1
     for (int j = 0; j < 4; ++j) {
       uint32_t o[32], h[16];
       tmem_ld32(tO + 32 * j, o);
@@ -696,6 +719,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_init(&sh.empty[i], 2);
       }
       bar_init(&sh.zeroed, 1);
+      for (int i = 0; i < 2; ++i) {
+        bar_init(&sh.block[i], 1);
+        bar_init(&sh.block_read[i], kReaders);
+      }
       sh.abort = 0;
       asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -717,6 +744,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_role(maps, cta, sh, lane);
     else if (warp < kLoadWarp)
       mma_role(cta, sh, warp - kMmaWarp, lane);
+    else
+      block_role(cta, sh, lane);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
     softmax_role(a, cta, sh, warp >> 2, warp & 3, lane);

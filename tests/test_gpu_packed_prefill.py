@@ -134,7 +134,7 @@ def test_attention_ignores_the_neighbours_values(poison):
     check_attention(out, q, k, v, cu, 0.1, seqs=[0, 2, 3])
 
 
-@pytest.mark.parametrize("kind", ["rising", "falling", "spike", "equal", "large", "zero-q"])
+@pytest.mark.parametrize("kind", ["rising", "falling", "spike", "equal", "large", "huge", "zero-q"])
 def test_attention_score_patterns(kind):
     """Running maxima that grow at every tile, never, or once; one-hot and uniform rows."""
     lens = [700, 130]
@@ -152,6 +152,12 @@ def test_attention_score_patterns(kind):
     elif kind == "large":
         q.mul_(30)
         k.mul_(30)
+    elif kind == "huge":  # scores of 2^25 and more, small integers apart
+        q.zero_()
+        q[:, :, 0], q[:, :, 1] = 32768.0, 16.0
+        k.zero_()
+        k[:, :, 0] = 16384.0
+        k[:, :, 1] = torch.randint(-3, 4, k[:, :, 1].shape, device="cuda").to(torch.float16)
     else:
         q.zero_()
     scale = 0.1
