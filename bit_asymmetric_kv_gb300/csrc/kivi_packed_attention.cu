@@ -26,10 +26,10 @@
 //   warp 11         finds the CTA's next block, one ahead.
 // Tensor memory: S/P of A and B (128 columns each), O of A and B (128 each): all 512.
 //
-// The maximum that the probabilities are relative to may lag behind the true one by 2^8:
+// The maximum that the probabilities are relative to may lag behind the true one by 2^11:
 // only beyond that are the sums and the output in tensor memory rescaled, which
 // happens in the first tiles of a row and then hardly ever.  The probabilities are scaled by
-// 2^7 on top, so that they use fp16's range (at most 2^15; the smallest lie 2^31 below)
+// 2^4 on top, so that they use fp16's range (at most 2^15; the smallest lie 2^28 below)
 // and their rounding, 2^-11 of each, is the only one below fp32 before the output's.
 //
 // Rows behind a sequence's end share its last tiles.  As query rows they are computed and
@@ -63,8 +63,8 @@ constexpr int kTileBytes = kRows * kD * 2;  // 32 KB: two halves of 64 channels
 constexpr int kHalfBytes = kTileBytes / 2;  // 128 rows of 128 bytes, 128-byte swizzle
 constexpr int kStages = 4;                  // K and V tiles in flight
 constexpr int kMaxPack = 16;
-constexpr float kLag = 8.f;                 // log2 by which the reference maximum may lag
-constexpr float kShift = 7.f;               // log2 of the probabilities' scale
+constexpr float kLag = 11.f;                // log2 by which the reference maximum may lag
+constexpr float kShift = 4.f;              // log2 of the probabilities' scale
 constexpr float kFar = 1 << 16;             // |log2 score| from which an offset in fp32 (2^-8 there) is not enough
 constexpr float kLog2eP = 1.4426950408889634f;
 constexpr int kPolls = 1 << 22;             // of a wait, each suspended by the hardware for a while
@@ -597,6 +597,13 @@ __device__ __forceinline__ void softmax_role(const PackedAttentionArgs &a, const
       const bool diagonal = t == t0;
       bool fresh = q == 2 * t0;  // the maximum has to be found before the exponentials
       uint32_t p[32];
+      if (g == 1 && diagonal && __all_sync(0xffffffffu, last < 64)) {  // no row sees these keys
+#pragma unroll
+        for (int j = 0; j < 32; ++j) p[j] = 0;
+        put(g, p);
+        continue;
+      }
+      const bool cut = diagonal && __any_sync(0xffffffffu, last < 64 * g + 63);
       for (;;) {
         uint32_t s[64];
         tmem_ld32(tS + 64 * g, s);
@@ -604,7 +611,7 @@ __device__ __forceinline__ void softmax_role(const PackedAttentionArgs &a, const
         tc_wait_ld();
         landed32(s);
         landed32(s + 32);
-        if (diagonal) {
+        if (cut) {
 #pragma unroll
           for (int j = 0; j < 64; ++j)
             if (j + 64 * g > last) s[j] = 0xff800000u;
@@ -660,19 +667,21 @@ __device__ __forceinline__ void softmax_role(const PackedAttentionArgs &a, const
     uint16_t *dst = a.out.p + (int64_t)(w.start + token) * a.out.ts + (int64_t)(w.head0 + r / cta.tpt) * a.out.hs;
     const bool mine = token < w.len;
 #pragma unroll 1
-    for (int j = 0; j < 4; ++j) {
-      uint32_t o[32], h[16];
-      tmem_ld32(tO + 32 * j, o);
+    for (int j = 0; j < 2; ++j) {
+      uint32_t o[64];
+      tmem_ld32(tO + 64 * j, o);
+      tmem_ld32(tO + 64 * j + 32, o + 32);
       tc_wait_ld();
       landed32(o);
+      landed32(o + 32);
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        h[i] = half2_of(__float_as_uint(__uint_as_float(o[2 * i]) * inv), __float_as_uint(__uint_as_float(o[2 * i + 1]) * inv));
+      for (int i = 0; i < 32; ++i)
+        o[i] = half2_of(__float_as_uint(__uint_as_float(o[2 * i]) * inv), __float_as_uint(__uint_as_float(o[2 * i + 1]) * inv));
       if (mine) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint16_t *d = dst + 32 * j + 16 * i;
-          const uint32_t *v = h + 8 * i;
+        for (int i = 0; i < 4; ++i) {
+          uint16_t *d = dst + 64 * j + 16 * i;
+          const uint32_t *v = o + 8 * i;
           if (wide) {
             asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(d), "r"(v[0]), "r"(v[1]),
                          "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
