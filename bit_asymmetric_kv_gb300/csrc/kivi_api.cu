@@ -675,7 +675,6 @@ int kivi_paged_prefill_packed(const kivi_paged_dims *d, const kivi_paged_cache *
   if ((s = check_packed(d->B, cu_seqlens, n_tokens)) != KIVI_OK) return s;
   for (const kivi_rows *r : {k, v})
     if ((s = check_rows(r)) != KIVI_OK) return s;
-  if (d->Hkv > 65535) return KIVI_ERR_UNSUPPORTED;  // grid.y of the launch
   if (n_tokens == 0) return KIVI_OK;
   kivi::PackedQuantArgs a = {};
   a.k = packed_rows(k);

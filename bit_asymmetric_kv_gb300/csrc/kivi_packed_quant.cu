@@ -3,11 +3,15 @@
 //
 // The method is kivi_paged_prefill's (KIVI page, headline paragraph and section "Iddia
 // ve Gerceklik", paragraphs 2-3): keys per channel in G-token groups, the rest of a
-// sequence's last group kept in fp16, values per token.  One CTA of 4 warps takes 64
-// tokens of one (sequence, KV head), which lie in one page and hold whole key groups.
-// Thread (rh, cp) holds channels 2cp, 2cp + 1 of token rows 32 rh .. 32 rh + 31, so a
-// channel's min and max need no shuffle (G = 64 merges two threads); a row of values is
-// held by 4 lanes.
+// sequence's last group kept in fp16, values per token.  The work is dealt out in units of
+// 64 tokens of one (sequence, KV head), which lie in one page and hold whole key groups;
+// a CTA of 4 warps takes a run of neighbouring units (heads of the same tokens first), so
+// that the device's lengths are searched once a CTA.
+// Keys: warp w takes rows 32 (w / 2) .. + 31 and channels 64 (w % 2) .. + 63; lane
+// (t4, c8) holds the 16-byte chunk c8 (8 channels) of rows t4, t4 + 4, .., so that a
+// channel's min and max are two shuffle rounds (G = 64 merges two warps through shared memory),
+// and derives the parameters of channel pair t4 of its chunk.  Values: a row is held by 4
+// lanes.
 #include "kivi_device.cuh"
 #include "kivi_internal.h"
 #include "kivi_packed.cuh"
@@ -18,192 +22,305 @@ namespace {
 
 constexpr int kQUnit = 64, kQThreads = 128;
 
-// Unit `idx` (kQUnit tokens) of the sequences' units in order, sequences cut to `cap`
-// tokens: lane i sums the units of 16 consecutive sequences, a warp scan finds the
-// lane, its own sequences the unit.  Every lane of a warp calls it.
-__device__ __forceinline__ bool packed_unit(const int32_t *cu, int n_seqs, int T, int cap, unsigned idx,
-                                            PackedBlock *out) {
-  constexpr int kPer = kPackedMaxSeqs / 32;
-  const int lane = threadIdx.x & 31;
-  const int per = (n_seqs + 31) / 32;
-  int nu[kPer], sum = 0;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    nu[k] = 0;
-    if (k < per) {
+constexpr int kQGrid = 152 * 5;  // CTAs: five fit on an SM (registers)
+
+// Where a run of units stands.
+struct UnitWalk {
+  const int32_t *cu;
+  int n_seqs, T, cap;
+  int seq, start, len, t0;  // sequence, its first row, its tokens (cut to the capacity), the unit's first
+
+  __device__ __forceinline__ void at(int s) {
+    seq = s;
+    packed_bounds(cu, s, T, &start, &len);
+    len = min(len, cap);
+    t0 = 0;
+  }
+  // The next unit; there is one.
+  __device__ __forceinline__ void next() {
+    t0 += kQUnit;
+    while (t0 >= len && seq + 1 < n_seqs) at(seq + 1);
+  }
+  // Every lane of a warp calls it: the units of all sequences.  Lane i sums those of `per`
+  // neighbouring sequences.
+  __device__ __forceinline__ int64_t begin(int *incl, int *mine) {
+    const int lane = threadIdx.x & 31, per = (n_seqs + 31) / 32;
+    int sum = 0;
+    for (int k = 0; k < per; ++k) {
       const int s = lane * per + k;
       if (s < n_seqs) {
-        int start, len;
-        packed_bounds(cu, s, T, &start, &len);
-        nu[k] = (min(len, cap) + kQUnit - 1) / kQUnit;
-        sum += nu[k];
+        int a, m;
+        packed_bounds(cu, s, T, &a, &m);
+        sum += (min(m, cap) + kQUnit - 1) / kQUnit;
       }
     }
-  }
-  int incl = sum;
+    *mine = sum;
+    int in = sum;
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += o;
-  }
-  const uint32_t past = __ballot_sync(0xffffffffu, (unsigned)incl > idx);
-  if (past == 0) return false;
-  const int owner = __ffs(past) - 1;
-  int rest = (int)idx - (incl - sum), seq = 0;
-  bool found = false;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    if (k < per && !found) {
-      if (rest < nu[k]) {
-        found = true;
-        seq = lane * per + k;
-      } else {
-        rest -= nu[k];
-      }
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, in, off);
+      if (lane >= off) in += o;
     }
+    *incl = in;
+    // bounds that overlap can pass any count: cut at what lengths that do not overlap can reach
+    return min((int64_t)T / kQUnit + n_seqs, (int64_t)max(__shfl_sync(0xffffffffu, in, 31), 0));
   }
-  seq = __shfl_sync(0xffffffffu, seq, owner);
-  rest = __shfl_sync(0xffffffffu, rest, owner);
-  if (seq >= n_seqs || rest < 0) return false;
-  out->seq = seq;
-  packed_bounds(cu, seq, T, &out->start, &out->len);
-  out->len = min(out->len, cap);
-  out->level = rest;
-  return (int64_t)rest * kQUnit < out->len;
-}
+  // To unit `idx` < begin(): a scan over the warp finds the lane, its sequences the unit.
+  __device__ __forceinline__ void find(int64_t idx, int incl, int mine) {
+    const int per = (n_seqs + 31) / 32;
+    const uint32_t past = __ballot_sync(0xffffffffu, (int64_t)incl > idx);
+    const int owner = past ? __ffs(past) - 1 : 31;
+    int rest = (int)(idx - __shfl_sync(0xffffffffu, incl - mine, owner));
+    int s = owner * per;
+    at(min(s, n_seqs - 1));
+    while (rest >= (len + kQUnit - 1) / kQUnit && seq + 1 < n_seqs) {
+      rest -= (len + kQUnit - 1) / kQUnit;
+      at(seq + 1);
+    }
+    t0 = rest * kQUnit;
+  }
+};
 
 template <int BITS>
-__global__ void __launch_bounds__(kQThreads) packed_quantize_kernel(const PackedQuantArgs a) {
+__global__ void __launch_bounds__(kQThreads, 5) packed_quantize_kernel(const PackedQuantArgs a) {
   constexpr int WPR = words_per_row<BITS>();
-  constexpr int LPW = 16 / BITS;  // channel pairs per packed word
   __shared__ uint2 s_mm[kQThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.y, G = a.G;
-  PackedBlock blk;
-  if (!packed_unit(a.cu, a.B, a.T, a.max_pages << a.shift, blockIdx.x, &blk)) return;
-  const int b = blk.seq, n = blk.len, t0 = blk.level * kQUnit;
-  const int nq = n / G * G, rows = min(kQUnit, n - t0);
-  const int nv = a.v_res ? nq : n;  // values quantized token by token
-  if (t0 == 0 && h == 0 && tid == 0) a.seq_lens[b] = n;
-  const uint16_t *ks = a.k.p + (int64_t)(blk.start + t0) * a.k.ts + (int64_t)h * a.k.hs;
-  const uint16_t *vs = a.v.p + (int64_t)(blk.start + t0) * a.v.ts + (int64_t)h * a.v.hs;
-  const int64_t page = a.bt[(int64_t)b * a.max_pages + (t0 >> a.shift)];
-  const bool paged = page >= 0 && page < a.num_pages;
-  // first row of the unit in the pool (the first page when the table gives none: not written)
-  const int64_t row0 = (((paged ? page : 0) * a.Hkv + h) << a.shift) + (t0 & ((1 << a.shift) - 1));
+  const int G = a.G;
+  UnitWalk u = {a.cu, a.B, a.T, a.max_pages << a.shift, 0, 0, 0, 0};
+  int incl, mine;
+  const int64_t items = u.begin(&incl, &mine) * a.Hkv;
+  const int64_t first = items * blockIdx.x / gridDim.x, end = items * (blockIdx.x + 1) / gridDim.x;
+  if (first >= end) return;
+  u.find(first / a.Hkv, incl, mine);
+  int h = (int)(first % a.Hkv);
+  for (int64_t item = first; item < end; ++item, ++h) {
+    if (h == a.Hkv) {
+      h = 0;
+      u.next();
+    }
+    const int b = u.seq, n = u.len, t0 = u.t0;
+    if ((unsigned)t0 >= (unsigned)n) return;  // only where bounds overlap
+    const int nq = n / G * G, rows = min(kQUnit, n - t0);
+    const int nv = a.v_res ? nq : n;  // values quantized token by token
+    if (t0 == 0 && h == 0 && tid == 0) a.seq_lens[b] = n;
+    const uint16_t *ks = a.k.p + (int64_t)(u.start + t0) * a.k.ts + (int64_t)h * a.k.hs;
+    const uint16_t *vs = a.v.p + (int64_t)(u.start + t0) * a.v.ts + (int64_t)h * a.v.hs;
+    const int64_t page = a.bt[(int64_t)b * a.max_pages + (t0 >> a.shift)];
+    const bool paged = page >= 0 && page < a.num_pages;
+    // first row of the unit in the pool (the first page when the table gives none: not written)
+    const int64_t row0 = (((paged ? page : 0) * a.Hkv + h) << a.shift) + (t0 & ((1 << a.shift) - 1));
 
-  // ---- all loads of the unit: keys by column pair, values by row
-  const int cp = tid & 63, rh = tid >> 6;
-  uint32_t x[32];
+    // ---- all loads of the unit
+    const int rh = warp >> 1, ch = warp & 1, t4 = lane >> 3, c8 = lane & 7;
+    uint32_t x[8][4];
 #pragma unroll
-  for (int r = 0; r < 32; ++r) {
-    const int row = 32 * rh + r;
-    x[r] = row < rows ? __ldg(reinterpret_cast<const uint32_t *>(ks + (int64_t)row * a.k.ts) + cp) : 0u;
-  }
-  const int q = lane & 3;
-  uint4 y[2][4];
+    for (int k = 0; k < 8; ++k) {
+      const int row = 32 * rh + t4 + 4 * k;
+      const uint4 c = row < rows ? __ldg(reinterpret_cast<const uint4 *>(ks + (int64_t)row * a.k.ts) + 8 * ch + c8)
+                                 : make_uint4(0u, 0u, 0u, 0u);
+      x[k][0] = c.x;
+      x[k][1] = c.y;
+      x[k][2] = c.z;
+      x[k][3] = c.w;
+    }
+    const int q = lane & 3;
+    uint4 y[2][4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int row = 32 * i + 8 * warp + (lane >> 2);
+    for (int i = 0; i < 2; ++i) {
+      const int row = 32 * i + 8 * warp + (lane >> 2);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      y[i][k] = row < rows ? __ldg(reinterpret_cast<const uint4 *>(vs + (int64_t)row * a.v.ts) + q + 4 * k)
-                           : make_uint4(0u, 0u, 0u, 0u);
-  }
-  // ---- key groups
-  __half2 mn = u2h2(x[0]), mx = mn;
+      for (int k = 0; k < 4; ++k)
+        y[i][k] = row < rows ? __ldg(reinterpret_cast<const uint4 *>(vs + (int64_t)row * a.v.ts) + q + 4 * k)
+                             : make_uint4(0u, 0u, 0u, 0u);
+    }
+    // ---- key groups
+    __half2 mn[4], mx[4];
 #pragma unroll
-  for (int r = 1; r < 32; ++r) {
-    mn = __hmin2(mn, u2h2(x[r]));
-    mx = __hmax2(mx, u2h2(x[r]));
-  }
-  if (G == 64) {  // uniform over the CTA
-    s_mm[tid] = make_uint2(h22u(mn), h22u(mx));
-    __syncthreads();
-    const uint2 o = s_mm[tid ^ 64];
-    mn = __hmin2(mn, u2h2(o.x));
-    mx = __hmax2(mx, u2h2(o.y));
-  }
-  const int g0 = G == 32 ? 32 * rh : 0;               // first row of this thread's group in the unit
-  const bool whole = paged && t0 + g0 + G <= nq;      // a quantized group (not the residual)
-  key_pair_codes<BITS>(x, mn, mx, lane, whole, G == 32 || rh == 0, a.k_meta + ((row0 + g0) / G) * kD + 2 * cp,
-                       a.k_codes + (row0 + 32 * rh) * WPR + cp / LPW);
-  // ---- the residual: rows nq .. n - 1 that lie in this unit
-  for (int it = tid; it < kQUnit * (kD / 8); it += kQThreads) {
-    const int r = it / (kD / 8), ch = it % (kD / 8);
-    if (t0 + r < nq || r >= rows) continue;
-    const int64_t dst = (((int64_t)b * a.Hkv + h) * G + (t0 + r - nq)) * kD + 8 * ch;
-    *reinterpret_cast<uint4 *>(a.k_res + dst) = __ldg(reinterpret_cast<const uint4 *>(ks + (int64_t)r * a.k.ts) + ch);
-    if (a.v_res)
-      *reinterpret_cast<uint4 *>(a.v_res + dst) = __ldg(reinterpret_cast<const uint4 *>(vs + (int64_t)r * a.v.ts) + ch);
-  }
-  // ---- value rows: lane q of a row holds chunks q + 4k (8 channels each)
+    for (int j = 0; j < 4; ++j) {
+      mn[j] = mx[j] = u2h2(x[0][j]);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = 32 * i + 8 * warp + (lane >> 2);
-    const bool ok_row = paged && t0 + r < nv;
-    __half2 vmn = u2h2(y[i][0].x), vmx = vmn;
+      for (int k = 1; k < 8; ++k) {
+        mn[j] = __hmin2(mn[j], u2h2(x[k][j]));
+        mx[j] = __hmax2(mx[j], u2h2(x[k][j]));
+      }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t w[4] = {y[i][k].x, y[i][k].y, y[i][k].z, y[i][k].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        vmn = __hmin2(vmn, u2h2(w[j]));
-        vmx = __hmax2(vmx, u2h2(w[j]));
+      for (int off = 8; off < 32; off <<= 1) {
+        mn[j] = __hmin2(mn[j], u2h2(__shfl_xor_sync(0xffffffffu, h22u(mn[j]), off)));
+        mx[j] = __hmax2(mx[j], u2h2(__shfl_xor_sync(0xffffffffu, h22u(mx[j]), off)));
       }
     }
-    // (min, -max) so that one __hmin2 reduces both over the row's 4 lanes
-    __half2 red = __halves2half2(__hmin(__low2half(vmn), __high2half(vmn)),
-                                 __hneg(__hmax(__low2half(vmx), __high2half(vmx))));
-    red = __hmin2(red, u2h2(__shfl_xor_sync(0xffffffffu, h22u(red), 1)));
-    red = __hmin2(red, u2h2(__shfl_xor_sync(0xffffffffu, h22u(red), 2)));
-    const QParams p = make_qparams<BITS>(__low2float(red), -__high2float(red));
-    uint32_t *codes_row = a.v_codes + (row0 + r) * WPR;
-    if constexpr (BITS == 4) {
-      if (ok_row) {
+    // this lane's channel pair: t4 of the chunk (channels 8 c8 + 2 t4, + 1)
+    __half2 pmn = mn[0], pmx = mx[0];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) codes_row[q + 4 * k] = qchunk8<4>(y[i][k], p);
+    for (int j = 1; j < 4; ++j)
+      if (t4 == j) {
+        pmn = mn[j];
+        pmx = mx[j];
       }
-    } else {
-      // lane q < 3 proves threshold q + 1 of the row (the second is the strict one)
-      bool ok = true;
-      uint32_t xq = 0x7c00u;
-      if (p.s != 0.f && q < 3) xq = fp16_threshold(p.mn, q == 0 ? p.t1 : (q == 1 ? p.t2 : p.t3), q == 1, ok);
-      const int base = lane & ~3;
-      const uint32_t x1 = __shfl_sync(0xffffffffu, xq, base), x2 = __shfl_sync(0xffffffffu, xq, base + 1),
-                     x3 = __shfl_sync(0xffffffffu, xq, base + 2);
-      uint32_t c[4];
-      if (__all_sync(0xffffffffu, ok)) {
-        const uint32_t p1 = x1 | (x1 << 16), p2 = x2 | (x2 << 16), p3 = x3 | (x3 << 16);
-        const uint32_t X1[4] = {p1, p1, p1, p1}, X2[4] = {p2, p2, p2, p2}, X3[4] = {p3, p3, p3, p3};
+    if (G == 64) {  // uniform over the CTA
+      __syncthreads();  // the unit before has read its own
+      s_mm[tid] = make_uint2(h22u(pmn), h22u(pmx));
+      __syncthreads();
+      const uint2 o = s_mm[tid ^ 64];
+      pmn = __hmin2(pmn, u2h2(o.x));
+      pmx = __hmax2(pmx, u2h2(o.y));
+    }
+    const int g0 = G == 32 ? 32 * rh : 0;           // first row of the warp's group in the unit
+    if (paged && t0 + g0 + G <= nq) {               // a quantized group (not the residual)
+      const QParams p0 = make_qparams<BITS>(__low2float(pmn), __low2float(pmx));
+      const QParams p1 = make_qparams<BITS>(__high2float(pmn), __high2float(pmx));
+      if (G == 32 || rh == 0)
+        *reinterpret_cast<uint2 *>(a.k_meta + ((row0 + g0) / G) * kD + 64 * ch + 8 * c8 + 2 * t4) =
+            make_uint2(p0.meta, p1.meta);
+      uint32_t *codes = a.k_codes + (row0 + 32 * rh + t4) * WPR;
+      if constexpr (BITS == 4) {
+        // every channel of the chunk: pair j from lane 8 j + c8 (1/s, 0 where s = 0)
+        const float rs0 = p0.s == 0.f ? 0.f : __frcp_rn(p0.s), rs1 = p1.s == 0.f ? 0.f : __frcp_rn(p1.s);
+        float2 cmn[4], cs[4], crs[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t w[4] = {y[i][k].x, y[i][k].y, y[i][k].z, y[i][k].w};
-          c[k] = codes2_chunk8(w, X1, X2, X3);
+        for (int j = 0; j < 4; ++j) {
+          const int sl = 8 * j + c8;
+          cmn[j] = make_float2(__shfl_sync(0xffffffffu, p0.mn, sl), __shfl_sync(0xffffffffu, p1.mn, sl));
+          cs[j] = make_float2(__shfl_sync(0xffffffffu, p0.s, sl), __shfl_sync(0xffffffffu, p1.s, sl));
+          crs[j] = make_float2(__shfl_sync(0xffffffffu, rs0, sl), __shfl_sync(0xffffffffu, rs1, sl));
+        }
+        // chunk c8 of channel half ch is word 8 ch + c8 of a token row
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          uint32_t word = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) word |= code4x2(__half22float2(u2h2(x[k][j])), cmn[j], cs[j], crs[j]) << (8 * j);
+          codes[4 * k * WPR + 8 * ch + c8] = word;
         }
       } else {
+        uint32_t a1, a2, a3, b1, b2, b3;
+        bool oa, ob;
+        fp16_thresholds(p0, a1, a2, a3, oa);
+        fp16_thresholds(p1, b1, b2, b3, ob);
+        uint32_t r[8];
+        if (__all_sync(0xffffffffu, oa && ob)) {
+          const uint32_t P1 = a1 | (b1 << 16), P2 = a2 | (b2 << 16), P3 = a3 | (b3 << 16);
+          uint32_t T1[4], T2[4], T3[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) c[k] = quant_chunk8<2>(y[i][k], p);
-      }
-      // word w = chunk 2w | chunk 2w + 1 << 16: lanes q, q ^ 1 hold the halves of words
-      // q / 2 + 2k; the even lane stores k = 0, 1, the odd one k = 2, 3
-      const uint32_t A = __byte_perm(c[0], c[1], 0x5410), B = __byte_perm(c[2], c[3], 0x5410);
-      const uint32_t recv = __shfl_xor_sync(0xffffffffu, (q & 1) ? A : B, 1);
-      const uint32_t lo = (q & 1) ? recv : A, hi = (q & 1) ? B : recv;
-      if (ok_row) {
-        const int w = (q >> 1) + ((q & 1) ? 4 : 0);
-        codes_row[w] = __byte_perm(lo, hi, 0x5410);
-        codes_row[w + 2] = __byte_perm(lo, hi, 0x7632);
+          for (int j = 0; j < 4; ++j) {  // pair j of the chunk lives in lane 8 j + c8
+            T1[j] = __shfl_sync(0xffffffffu, P1, 8 * j + c8);
+            T2[j] = __shfl_sync(0xffffffffu, P2, 8 * j + c8);
+            T3[j] = __shfl_sync(0xffffffffu, P3, 8 * j + c8);
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) r[k] = codes2_chunk8(x[k], T1, T2, T3);
+        } else {
+          // the fp32 comparison form with every channel's parameters of the chunk
+          float qm[8], q1[8], q2[8], q3[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int sl = 8 * (j / 2) + c8;
+            const QParams &p = j & 1 ? p1 : p0;
+            qm[j] = __shfl_sync(0xffffffffu, p.mn, sl);
+            q1[j] = __shfl_sync(0xffffffffu, p.t1, sl);
+            q2[j] = __shfl_sync(0xffffffffu, p.t2, sl);
+            q3[j] = __shfl_sync(0xffffffffu, p.t3, sl);
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            r[k] = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float d = __fsub_rn(h2f((uint16_t)(x[k][j / 2] >> (16 * (j & 1)))), qm[j]);
+              r[k] |= ((uint32_t)(d > q1[j]) + (uint32_t)(d >= q2[j]) + (uint32_t)(d > q3[j])) << (2 * j);
+            }
+          }
+        }
+        // chunks 2m and 2m + 1 (lanes c8, c8 ^ 1) are the halves of word 4 ch + m of a token
+        // row: the even lane stores rows t4 + 8 i, the odd one rows t4 + 8 i + 4
+        const bool odd = c8 & 1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? r[2 * i] : r[2 * i + 1], 1);
+          const uint32_t lo = odd ? got : r[2 * i], hi = odd ? r[2 * i + 1] : got;
+          codes[(8 * i + (odd ? 4 : 0)) * WPR + 4 * ch + (c8 >> 1)] = __byte_perm(lo, hi, 0x5410);
+        }
       }
     }
-    if (ok_row && q == 0) a.v_meta[row0 + r] = p.meta;
+    // ---- the residual: rows nq .. n - 1 that lie in this unit
+    for (int it = tid; it < (t0 + rows > nq ? kQUnit * (kD / 8) : 0); it += kQThreads) {
+      const int r = it / (kD / 8), ch = it % (kD / 8);
+      if (t0 + r < nq || r >= rows) continue;
+      const int64_t dst = (((int64_t)b * a.Hkv + h) * G + (t0 + r - nq)) * kD + 8 * ch;
+      *reinterpret_cast<uint4 *>(a.k_res + dst) = __ldg(reinterpret_cast<const uint4 *>(ks + (int64_t)r * a.k.ts) + ch);
+      if (a.v_res)
+        *reinterpret_cast<uint4 *>(a.v_res + dst) = __ldg(reinterpret_cast<const uint4 *>(vs + (int64_t)r * a.v.ts) + ch);
+    }
+    // ---- value rows: lane q of a row holds chunks q + 4k (8 channels each)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 32 * i + 8 * warp + (lane >> 2);
+      const bool ok_row = paged && t0 + r < nv;
+      __half2 vmn = u2h2(y[i][0].x), vmx = vmn;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t w[4] = {y[i][k].x, y[i][k].y, y[i][k].z, y[i][k].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          vmn = __hmin2(vmn, u2h2(w[j]));
+          vmx = __hmax2(vmx, u2h2(w[j]));
+        }
+      }
+      // (min, -max) so that one __hmin2 reduces both over the row's 4 lanes
+      __half2 red = __halves2half2(__hmin(__low2half(vmn), __high2half(vmn)),
+                                   __hneg(__hmax(__low2half(vmx), __high2half(vmx))));
+      red = __hmin2(red, u2h2(__shfl_xor_sync(0xffffffffu, h22u(red), 1)));
+      red = __hmin2(red, u2h2(__shfl_xor_sync(0xffffffffu, h22u(red), 2)));
+      const QParams p = make_qparams<BITS>(__low2float(red), -__high2float(red));
+      uint32_t *codes_row = a.v_codes + (row0 + r) * WPR;
+      if constexpr (BITS == 4) {
+        if (ok_row) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) codes_row[q + 4 * k] = qchunk8<4>(y[i][k], p);
+        }
+      } else {
+        // lane q < 3 proves threshold q + 1 of the row (the second is the strict one)
+        bool ok = true;
+        uint32_t xq = 0x7c00u;
+        if (p.s != 0.f && q < 3) xq = fp16_threshold(p.mn, q == 0 ? p.t1 : (q == 1 ? p.t2 : p.t3), q == 1, ok);
+        const int base = lane & ~3;
+        const uint32_t x1 = __shfl_sync(0xffffffffu, xq, base), x2 = __shfl_sync(0xffffffffu, xq, base + 1),
+                       x3 = __shfl_sync(0xffffffffu, xq, base + 2);
+        uint32_t c[4];
+        if (__all_sync(0xffffffffu, ok)) {
+          const uint32_t p1 = x1 | (x1 << 16), p2 = x2 | (x2 << 16), p3 = x3 | (x3 << 16);
+          const uint32_t X1[4] = {p1, p1, p1, p1}, X2[4] = {p2, p2, p2, p2}, X3[4] = {p3, p3, p3, p3};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t w[4] = {y[i][k].x, y[i][k].y, y[i][k].z, y[i][k].w};
+            c[k] = codes2_chunk8(w, X1, X2, X3);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) c[k] = quant_chunk8<2>(y[i][k], p);
+        }
+        // word w = chunk 2w | chunk 2w + 1 << 16: lanes q, q ^ 1 hold the halves of words
+        // q / 2 + 2k; the even lane stores k = 0, 1, the odd one k = 2, 3
+        const uint32_t A = __byte_perm(c[0], c[1], 0x5410), B = __byte_perm(c[2], c[3], 0x5410);
+        const uint32_t recv = __shfl_xor_sync(0xffffffffu, (q & 1) ? A : B, 1);
+        const uint32_t lo = (q & 1) ? recv : A, hi = (q & 1) ? B : recv;
+        if (ok_row) {
+          const int w = (q >> 1) + ((q & 1) ? 4 : 0);
+          codes_row[w] = __byte_perm(lo, hi, 0x5410);
+          codes_row[w + 2] = __byte_perm(lo, hi, 0x7632);
+        }
+      }
+      if (ok_row && q == 0) a.v_meta[row0 + r] = p.meta;
+    }
   }
 }
 
 }  // namespace
 
 cudaError_t launch_packed_quantize(const PackedQuantArgs &a, cudaStream_t st) {
-  const dim3 grid((unsigned)(a.T / kQUnit + a.B), (unsigned)a.Hkv);
+  const int64_t items = ((int64_t)a.T / kQUnit + a.B) * a.Hkv;
+  const unsigned grid = (unsigned)(items < kQGrid ? items : kQGrid);
   if (a.bits == 2)
     packed_quantize_kernel<2><<<grid, kQThreads, 0, st>>>(a);
   else

@@ -427,8 +427,7 @@ KIVI_API int kivi_prefill_attention_packed(int32_t Hq, int32_t Hkv, int32_t D, i
  * one: codes, scales, zeros and residual bit for bit, and seq_lens[s] = its length.  An
  * empty sequence leaves sequence s of the cache as it is.  Tokens at or beyond
  * max_pages_per_seq * P are dropped, and so are those of a position whose table entry
- * lies outside the pool (the length still counts the latter).  Hkv <= 65535
- * (KIVI_ERR_UNSUPPORTED).
+ * lies outside the pool (the length still counts the latter).
  */
 KIVI_API int kivi_paged_prefill_packed(const kivi_paged_dims *dims, const kivi_paged_cache *cache,
                                        const int32_t *cu_seqlens, int64_t n_tokens, const kivi_rows *k,

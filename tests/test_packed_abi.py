@@ -61,7 +61,7 @@ def _cache(table=FAKE, v_res=0):
 
 @pytest.mark.parametrize("bad,status", [
     (dict(dims=_dims(B=0)), 1), (dict(dims=_dims(G=48)), 3), (dict(dims=_dims(page_tokens=96)), 3),
-    (dict(dims=_dims(Hkv=65536)), 3), (dict(dims=_dims(value_residual=1)), 1), (dict(cache=_cache(table=0)), 1),
+    (dict(dims=_dims(value_residual=1)), 1), (dict(cache=_cache(table=0)), 1),
     (dict(cu=0), 1), (dict(cu=FAKE + 1), 2), (dict(T=-1), 1), (dict(T=1 << 31), 3), (dict(k=_rows(0)), 1),
     (dict(v=_rows(FAKE + 2)), 2), (dict(k=_rows(ts=4)), 1), (dict(v=_rows(hs=129)), 2),
 ])
