@@ -201,6 +201,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
     const int m = entries(b0 + i);
     const int32_t *row = a.bt + (int64_t)(b0 + i) * a.max_pages;
     int c = 0;
+#pragma unroll 4
     for (int j = lane; j < m; j += 32) c += !in_pool(a, row[j]);
     c = __reduce_add_sync(0xffffffffu, c);
     if (lane == 0) s_rank[i] = c;
@@ -224,13 +225,18 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
     const int m = entries(b0 + i);
     int32_t *row = a.bt + (int64_t)(b0 + i) * a.max_pages;
     int k = s_rank[i];
-    for (int j0 = 0; j0 < m; j0 += 32) {
-      const int j = j0 + lane;
-      const bool want = j < m && !in_pool(a, row[j]);
-      const uint32_t mask = __ballot_sync(0xffffffffu, want);
-      const int mine = k + __popc(mask & ((1u << lane) - 1u));
-      if (want) row[j] = mine < got ? __ldcg(ws.list + mine) : -1;
-      k += __popc(mask);
+    for (int j0 = 0; j0 < m; j0 += 128) {  // four loads in flight
+      int page[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) page[u] = j0 + 32 * u + lane < m ? row[j0 + 32 * u + lane] : 0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool want = !in_pool(a, page[u]);  // page 0 past the end is one
+        const uint32_t mask = __ballot_sync(0xffffffffu, want);
+        const int mine = k + __popc(mask & ((1u << lane) - 1u));
+        if (want) row[j0 + 32 * u + lane] = mine < got ? __ldcg(ws.list + mine) : -1;
+        k += __popc(mask);
+      }
     }
   }
   if (r == 0 && threadIdx.x == 0) {
@@ -244,14 +250,13 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
 // ------------------------------------------------------------------------- reorder
 __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads)
     pool_reorder_kernel(const PoolArgs a, const Ws ws) {
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   __shared__ Shared sh;
   __shared__ int s_parent[kPagedMaxBatch], s_first[kPagedMaxBatch], s_len[kPagedMaxBatch];
   __shared__ int s_rank[kPagedMaxBatch], s_from[kPagedMaxBatch];
-  __shared__ int s_dead;
   cg::cluster_group cl = cg::this_cluster();
   const int r = (int)cl.block_rank(), tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int B = a.B, P = 1 << a.shift;
-  if (tid == 0) s_dead = 0;
   for (int b = tid; b < B; b += kPoolThreads) {
     const int p = a.arg[b];
     s_parent[b] = p >= 0 && p < B ? p : -1;
@@ -281,35 +286,46 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   const int rank = block_scan(want, sh, &wanted);
   if (tid < B) s_rank[tid] = rank;
   __syncthreads();
+  int lo, hi;
+  slice(r, a.num_pages, &lo, &hi);
+  auto is_free = [](int c, int) { return c <= 0; };
+  const int before = count_slice(a.refs, lo, hi, 1, sh, is_free);
+  cl.sync();  // every count has been read
   // ---- the new rows, staged, and the counts of the pages that rows lose and gain
   const int per = (B + kPoolCtas - 1) / kPoolCtas;
   const int b0 = min(B, per * r), b1 = min(B, b0 + per);
-  int dead = 0;
   for (int b = b0 + w; b < b1; b += kPoolWarps) {
     const int s = s_parent[b];
     if (s == b) continue;
     const int32_t *old = a.bt + (int64_t)b * a.max_pages;
     const int32_t *src = s >= 0 ? a.bt + (int64_t)s * a.max_pages : old;
     const int shared = s < 0 ? 0 : (heir(s) == b ? a.max_pages : s_len[s] / P);
-    for (int j = lane; j < a.max_pages; j += 32) {
-      int o = old[j], n = j < shared ? src[j] : -1;
-      if (!in_pool(a, o)) o = -1;
-      if (!in_pool(a, n)) n = -1;
-      if (o != n) {
-        if (o >= 0) dead += atomicAdd(a.refs + o, -1) == 1;
-        if (n >= 0) dead -= atomicAdd(a.refs + n, 1) == 0;
+    for (int j0 = lane; j0 < a.max_pages; j0 += 128) {  // four loads of each in flight
+      int o[4], n[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int j = j0 + 32 * u;
+        o[u] = j < a.max_pages ? old[j] : -1;
+        n[u] = j < shared ? src[j] : -1;
       }
-      ws.table[(int64_t)b * a.max_pages + j] = n;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int j = j0 + 32 * u;
+        if (j >= a.max_pages) break;
+        if (!in_pool(a, o[u])) o[u] = -1;
+        if (!in_pool(a, n[u])) n[u] = -1;
+        if (o[u] != n[u]) {
+          if (o[u] >= 0) atomicAdd(a.refs + o[u], -1);
+          if (n[u] >= 0) atomicAdd(a.refs + n[u], 1);
+        }
+        ws.table[(int64_t)b * a.max_pages + j] = n[u];
+      }
     }
   }
-  if (dead) atomicAdd(&s_dead, dead);
   cl.sync();  // all old rows read, all counts changed
-  int lo, hi;
-  slice(r, a.num_pages, &lo, &hi);
-  auto is_free = [](int c, int) { return c <= 0; };
   const int nfree = count_slice(a.refs, lo, hi, 1, sh, is_free);
   Spread fr, gone;
-  exchange(cl, sh, nfree, s_dead, &fr, &gone);
+  exchange(cl, sh, nfree, nfree - before, &fr, &gone);
   const int got = min(fr.all, wanted);
   list_slice(a.refs, lo, hi, 1, sh, fr.before, got, is_free, [&](int k, int id) {
     ws.list[k] = id;
@@ -357,7 +373,16 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
 __device__ void copy16(void *dst, const void *src, int64_t bytes) {
   const uint4 *s = static_cast<const uint4 *>(src);
   uint4 *d = static_cast<uint4 *>(dst);
-  for (int64_t i = threadIdx.x; i < bytes / 16; i += blockDim.x) d[i] = s[i];
+  const int64_t n = bytes / 16;
+  for (int64_t i = threadIdx.x; i < n; i += 4 * blockDim.x) {
+    uint4 x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j * blockDim.x < n) x[j] = s[i + j * blockDim.x];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j * blockDim.x < n) d[i + j * blockDim.x] = x[j];
+  }
 }
 
 __device__ Plan plan_of(const Ws &ws, int b) {
@@ -369,6 +394,8 @@ __device__ Plan plan_of(const Ws &ws, int b) {
 // sequence does not share, and its residual rows where neither end is overwritten or
 // needed elsewhere; residuals that others need are copied aside.  Pass 1 copies the rest.
 __global__ void __launch_bounds__(128) pool_copy_kernel(const PoolArgs a, const Ws ws, int pass) {
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int h = blockIdx.x, b = blockIdx.y, P = 1 << a.shift, G = a.G;
   const Plan p = plan_of(ws, b);
   const int64_t head = ((int64_t)b * a.Hkv + h) * G * kD;
@@ -399,6 +426,7 @@ __global__ void __launch_bounds__(128) pool_copy_kernel(const PoolArgs a, const 
 // ------------------------------------------------------------------------- compact
 __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads)
     pool_compact_kernel(const PoolArgs a, const Ws ws) {
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   __shared__ Shared sh;
   cg::cluster_group cl = cg::this_cluster();
   const int r = (int)cl.block_rank();
@@ -436,22 +464,67 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   }
 }
 
-// Moved pages, one CTA a page at a time, and the table's entries.
-__global__ void __launch_bounds__(256) pool_move_kernel(const PoolArgs a, const Ws ws) {
-  const int n = ws.count[0];
-  const int64_t rows = (int64_t)a.Hkv << a.shift, W = 4 * a.bits;
-  for (int k = blockIdx.x; k < n; k += gridDim.x) {
-    const int64_t f = ws.from[k] * rows, t = ws.list[k] * rows;
-    copy16(a.k_codes + t * W, a.k_codes + f * W, rows * W * 4);
-    copy16(a.k_meta + t / a.G * kD, a.k_meta + f / a.G * kD, rows / a.G * kD * 4);
-    copy16(a.v_codes + t * W, a.v_codes + f * W, rows * W * 4);
-    copy16(a.v_meta + t, a.v_meta + f, rows * 4);
+// Moved pages, and the table's entries.  A warp copies pieces of 4 KB (8 x 16 bytes a lane in
+// flight: with 16 warps an SM, more than the memory's latency needs), so that pages of any
+// size keep every SM busy.
+constexpr int kMoveThreads = 256, kMoveGrid = 152 * 4, kPiece = 4096;
+
+__global__ void __launch_bounds__(kMoveThreads) pool_move_kernel(const PoolArgs a, const Ws ws) {
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const int n = ws.count[0], lane = threadIdx.x & 31;
+  const int64_t rows = (int64_t)a.Hkv << a.shift;  // of a page, all heads
+  const int64_t codes = rows * 4 * a.bits * 4, meta = rows / a.G * kD * 4, vmeta = rows * 4;
+  const int64_t pc = (codes + kPiece - 1) / kPiece, pm = (meta + kPiece - 1) / kPiece, pv = (vmeta + kPiece - 1) / kPiece;
+  const int64_t pieces = 2 * pc + pm + pv;
+  const int64_t warps = (int64_t)gridDim.x * (kMoveThreads / 32);
+  for (int64_t i = (int64_t)blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5); i < n * pieces; i += warps) {
+    const int64_t k = i / pieces;
+    int64_t piece = i - k * pieces, bytes = codes;
+    char *base = reinterpret_cast<char *>(a.k_codes);
+    if (piece >= 2 * pc + pm) {
+      piece -= 2 * pc + pm;
+      base = reinterpret_cast<char *>(a.v_meta);
+      bytes = vmeta;
+    } else if (piece >= 2 * pc) {
+      piece -= 2 * pc;
+      base = reinterpret_cast<char *>(a.k_meta);
+      bytes = meta;
+    } else if (piece >= pc) {
+      piece -= pc;
+      base = reinterpret_cast<char *>(a.v_codes);
+    }
+    const uint4 *from = reinterpret_cast<const uint4 *>(base + ws.from[k] * bytes + piece * kPiece) + lane;
+    uint4 *to = reinterpret_cast<uint4 *>(base + ws.list[k] * bytes + piece * kPiece) + lane;
+    const int left = (int)min((int64_t)kPiece, bytes - piece * kPiece) / 16 - lane;  // 16-byte words from this lane's on
+    uint4 x[kPiece / 512];
+#pragma unroll
+    for (int j = 0; j < kPiece / 512; ++j)
+      if (32 * j < left) x[j] = __ldcs(from + 32 * j);
+#pragma unroll
+    for (int j = 0; j < kPiece / 512; ++j)
+      if (32 * j < left) __stcs(to + 32 * j, x[j]);
   }
   const int64_t entries = (int64_t)a.B * a.max_pages;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < entries; i += (int64_t)gridDim.x * blockDim.x) {
     const int page = a.bt[i];
     a.bt[i] = in_pool(a, page) ? a.new_ids[page] : -1;
   }
+}
+
+// A launch that may start while the kernel before it on the stream still runs; the kernel
+// waits for that one's end (griddepcontrol.wait) before it reads anything.
+template <class... Args>
+cudaError_t launch_behind(void (*kernel)(Args...), dim3 grid, int threads, cudaStream_t st, Args... args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 Ws workspace_of(const PoolArgs &a) {
@@ -476,10 +549,7 @@ cudaError_t launch_pool_reorder(const PoolArgs &a, cudaStream_t st) {
   pool_reorder_kernel<<<kPoolCtas, kPoolThreads, 0, st>>>(a, ws);
   cudaError_t e = cudaGetLastError();
   const dim3 grid((unsigned)a.Hkv, (unsigned)a.B);
-  for (int pass = 0; pass < 2 && e == cudaSuccess; ++pass) {
-    pool_copy_kernel<<<grid, 128, 0, st>>>(a, ws, pass);
-    e = cudaGetLastError();
-  }
+  for (int pass = 0; pass < 2 && e == cudaSuccess; ++pass) e = launch_behind(pool_copy_kernel, grid, 128, st, a, ws, pass);
   return e;
 }
 
@@ -488,8 +558,7 @@ cudaError_t launch_pool_compact(const PoolArgs &a, cudaStream_t st) {
   pool_compact_kernel<<<kPoolCtas, kPoolThreads, 0, st>>>(a, ws);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  pool_move_kernel<<<152 * 4, 256, 0, st>>>(a, ws);
-  return cudaGetLastError();
+  return launch_behind(pool_move_kernel, dim3(kMoveGrid), kMoveThreads, st, a, ws);
 }
 
 }  // namespace kivi
