@@ -1,7 +1,6 @@
 // kivi_api.cu -- the C ABI (include/kivi.h): argument checks, then kernel launches.
 // Nothing here allocates device memory, synchronises with the host or keeps state.
 #include <cuda_runtime.h>
-#include <float.h>
 #include <stdint.h>
 
 #include "../../include/kivi.h"
@@ -650,7 +649,7 @@ int kivi_prefill_attention_packed(int32_t Hq, int32_t Hkv, int32_t D, int32_t n_
   for (const kivi_rows *r : {q, k, v, out})
     if ((s = check_rows(r)) != KIVI_OK) return s;
   if (!rows_apart(out, n_tokens, Hq)) return KIVI_ERR_ARG;
-  if (!(softmax_scale > 0.f) || !(softmax_scale <= FLT_MAX)) return KIVI_ERR_ARG;
+  if (!(softmax_scale > 0.f) || !(softmax_scale <= 0x1p127f)) return KIVI_ERR_ARG;
   kivi::PackedAttentionArgs a = {};
   a.q = packed_rows(q);
   a.k = packed_rows(k);

@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kQUnit = 64, kQThreads = 128;
 
+static_assert(kPackedMaxSeqs == kPagedMaxBatch, "a packed batch is a paged batch");
 constexpr int kQGrid = 152 * 5;  // CTAs: five fit on an SM (registers)
 
 // Where a run of units stands.

@@ -410,11 +410,14 @@ typedef struct {
  *   out_i = sum_{j <= i} softmax_j(softmax_scale * q_i . k_j) v_j
  * over rows j of the same sequence, k and v of KV head h / (Hq / Hkv).  q, out: Hq
  * heads; k, v: Hkv heads; Hq any multiple of Hkv; D = 128 (KIVI_ERR_UNSUPPORTED).
- * The rows of a sequence must be finite; softmax_scale must be positive and finite
+ * The rows of a sequence must be finite; softmax_scale must be positive and at most 2^127
  * (KIVI_ERR_ARG).  out's elements must not overlap one another (KIVI_ERR_ARG) or the
  * inputs.  Scores, running maximum and sum, and the output's accumulators are fp32;
  * the probabilities enter the P.V product in fp16.  n_tokens == 0 launches nothing.
- * Nothing is allocated, and no state is kept between calls.
+ * Nothing is allocated.  The first call on a device asks the CUDA runtime about the kernel
+ * (its registers, the device's SMs, the tensor-map encoder) and remembers the answer: make it
+ * before capturing calls in a CUDA graph.  Device faults: every wait of the kernel is
+ * bounded; rows whose wait runs out are NaN.
  */
 KIVI_API int kivi_prefill_attention_packed(int32_t Hq, int32_t Hkv, int32_t D, int32_t n_seqs,
                                            const int32_t *cu_seqlens, int64_t n_tokens, const kivi_rows *q,

@@ -115,13 +115,29 @@ def test_attention_heads_and_layouts(layout, Hq, Hkv):
     assert (out[:9] == 7).all() and (out[9 + sum(lens):] == 7).all()  # rows of no sequence
 
 
-def test_attention_writes_only_its_elements():
+@pytest.mark.parametrize("width,at", [(160, 16), (160, 8), (152, 8), (128, 0)])  # rows on 32 bytes, and on 16 only
+def test_attention_writes_only_its_elements(width, at):
     (q, k, v), cu = pack([90, 130], [4, 2, 2], "tokens", 3)
-    big = torch.full((222, 6, 160), 5.0, dtype=torch.float16, device="cuda")
-    kivi.kivi_prefill_attention_packed(q, k, v, cu, 0.1, out=big[1:221, 1:5, 16:144])
-    check_attention(big[1:221, 1:5, 16:144], q, k, v, cu, 0.1)
-    big[1:221, 1:5, 16:144] = 5.0
+    big = torch.full((222, 6, width), 5.0, dtype=torch.float16, device="cuda")
+    out = big[1:221, 1:5, at:at + D]
+    kivi.kivi_prefill_attention_packed(q, k, v, cu, 0.1, out=out)
+    check_attention(out, q, k, v, cu, 0.1)
+    out.fill_(5.0)
     assert (big == 5).all()
+
+
+@pytest.mark.parametrize("scale", [1e-30, 2.0**100, 2.0**127])
+def test_attention_extreme_scales(scale):
+    """Every weight the same; and the largest score alone."""
+    (q, k, v), cu = pack([150], [1, 1, 1], "tokens", 16)
+    out = kivi.kivi_prefill_attention_packed(q, k, v, cu, scale)
+    x = (q[:, 0].double() @ k[:, 0].double().t()).masked_fill(
+        torch.ones((150, 150), dtype=torch.bool, device="cuda").triu(1), -math.inf)
+    ref = torch.softmax(x * 1e9, -1) if scale > 1 else None
+    if ref is None:
+        ref = torch.ones_like(x).tril() / torch.arange(1, 151, device="cuda").double()[:, None]
+    # the weights are exact or 2^-11 off; the output is rounded once
+    assert (out[:, 0].double() - ref @ v[:, 0].double()).abs().max() <= 2 * 2.0**-11 * float(v.abs().max())
 
 
 @pytest.mark.parametrize("poison", [math.inf, -math.inf, math.nan])

@@ -36,6 +36,7 @@ def _attention(L, Hq=8, Hkv=2, D=128, n_seqs=3, cu=FAKE, T=100, q=None, k=None, 
     (dict(q=_rows(FAKE + 8)), 2), (dict(v=_rows(ts=1028)), 2), (dict(k=_rows(hs=132)), 2), (dict(k=_rows(hs=0)), 1),
     (dict(q=_rows(ts=-1024)), 1), (dict(v=_rows(ts=(1 << 38) + 8)), 3), (dict(v=_rows(hs=(1 << 38) + 8)), 3),
     (dict(scale=0.0), 1), (dict(scale=-0.1), 1), (dict(scale=math.inf), 1), (dict(scale=math.nan), 1),
+    (dict(scale=2.0**127 * 1.01), 1),
     (dict(out=_rows(ts=128, hs=128)), 1),        # every head of a token on the next token's first
     (dict(out=_rows(ts=1016, hs=128)), 1),       # the last head reaches into the next token
     (dict(out=_rows(ts=128, hs=99 * 128)), 1),   # the last token reaches into the next head
