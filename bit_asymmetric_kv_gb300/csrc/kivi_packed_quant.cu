@@ -12,6 +12,11 @@
 // channel's min and max are two shuffle rounds (G = 64 merges two warps through shared memory),
 // and derives the parameters of channel pair t4 of its chunk.  Values: a row is held by 4
 // lanes.
+// Measured on 16 prompts of up to 8192 tokens, 8 KV heads, G = 64: 45 us, 0.53 of the measured
+// copy bandwidth.  Bound by instructions: the scheduler issues on 52% of cycles at 20 warps an
+// SM, and the loads of a unit wait for the arithmetic of the one before.  Units found one by one by a CTA each
+// took 58 us, keys held as column pairs of 32 rows (packed by a transpose across lanes) too; four
+// CTAs an SM without spills take the same 45 us.
 #include "kivi_device.cuh"
 #include "kivi_internal.h"
 #include "kivi_packed.cuh"
