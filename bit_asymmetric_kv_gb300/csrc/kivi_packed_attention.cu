@@ -46,12 +46,13 @@
 // without the copies 0.97.  Tried and slower on the long prompts: two threads a row in 16
 // softmax warps (1.26x); tiles of 80 keys with P in columns of its own, so that the next
 // scores go out before P.V (1.07x and 1.22x); turns on the exponential unit (1.09x);
-// probabilities handed over once a pass (1.08x); one MMA warp for both tiles (1.03x).
+// probabilities handed over once a pass (1.08x); one MMA warp for both tiles (1.03x); MMAs
+// issued by a softmax warp (1.5x: it stands still until they are taken).
 // Short prompts are bound by the length of one block's chain: copies, scores, softmax, P.V and output,
 // about 6500 cycles where all keys fit one tile.
 //
 // Every wait is bounded: one that runs out (a copy that never completes) ends all roles
-// of the CTA, whose rows from then on are NaN.
+// of the CTA; the rows of its block are NaN, those of its later blocks not written.
 #include <cuda.h>
 #include <math.h>
 

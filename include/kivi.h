@@ -417,7 +417,8 @@ typedef struct {
  * Nothing is allocated.  The first call on a device asks the CUDA runtime about the kernel
  * (its registers, the device's SMs, the tensor-map encoder) and remembers the answer: make it
  * before capturing calls in a CUDA graph.  Device faults: every wait of the kernel is
- * bounded; rows whose wait runs out are NaN.
+ * bounded; when one runs out (a copy that never completes), the rows it was for are NaN and
+ * others may be left unwritten, instead of a hang.
  */
 KIVI_API int kivi_prefill_attention_packed(int32_t Hq, int32_t Hkv, int32_t D, int32_t n_seqs,
                                            const int32_t *cu_seqlens, int64_t n_tokens, const kivi_rows *q,
