@@ -6,12 +6,13 @@
 // sequence's last group kept in fp16, values per token.  The work is dealt out in units of
 // 64 tokens of one (sequence, KV head), which lie in one page and hold whole key groups;
 // a CTA of 4 warps takes a run of neighbouring units (heads of the same tokens first), so
-// that the device's lengths are searched once a CTA.
-// Keys and values of a unit are two passes of a CTA.  Keys: warp w takes rows 32 (w / 2) .. + 31 and channels 64 (w % 2) .. + 63; lane
+// that the device's lengths are searched once a CTA.  Keys and values of a unit are two
+// passes.  Keys: warp w takes rows 32 (w / 2) .. + 31 and channels 64 (w % 2) .. + 63; lane
 // (t4, c8) holds the 16-byte chunk c8 (8 channels) of rows t4, t4 + 4, .., so that a
-// channel's min and max are two shuffle rounds (G = 64 merges two warps through shared memory),
-// and derives the parameters of channel pair t4 of its chunk.  Values: a row is held by 4
-// lanes.
+// channel's min and max are two shuffle rounds (G = 64 merges two warps through shared
+// memory), and derives the parameters of channel pair t4 of its chunk.  Values: a row is
+// held by 4 lanes.
+//
 // Measured on 16 prompts of up to 8192 tokens, 8 KV heads, G = 64: 43 us, 0.55 of the measured
 // copy bandwidth.  Bound by instructions: the integer and comparison unit is busy for 53% of
 // the cycles, as is the scheduler, and waits for the first loads and for code that every warp

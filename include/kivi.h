@@ -448,7 +448,7 @@ KIVI_API int kivi_paged_prefill_packed(const kivi_paged_dims *dims, const kivi_p
  * the lowest free pages in the order of the sequences, and are asynchronous on the
  * stream; a batch of them can be captured in a CUDA graph.  ws: device workspace of at
  * least kivi_paged_pool_workspace_bytes(), 16-byte aligned, contents overwritten; calls
- * that may overlap need one each.  num_pages <= 2^30 (KIVI_ERR_UNSUPPORTED).
+ * that may overlap need one each.  The arrays of a call must not overlap one another.  num_pages <= 2^30 (KIVI_ERR_UNSUPPORTED).
  */
 typedef struct {
   int32_t *block_table;  /* the cache's (KIVI_ERR_ARG otherwise) */
