@@ -13,17 +13,17 @@
 // takes block after block, longest first, so that the next block's copies and first
 // products run under the last one's output.
 //
-// Roles (12 warps):
+// Roles (12 warps, the last idle: registers go by four warps):
 //   warps 0-3, 4-7  softmax of tile A, of tile B: a thread holds one row.  It reads the 128
 //                   scores from tensor memory, keeps the running maximum and sum, and
 //                   writes the probabilities over the scores, as fp16; at the end of a
 //                   block it divides the output by the sum and stores it.
-//   warps 8, 9      one lane issues the MMAs of tile A, of tile B: S = Q K^T (both operands in
-//                   shared memory) and O += P V (P in tensor memory); one tile's softmax
-//                   runs under the other's MMAs.
+//   warp 8          one lane issues the MMAs: S = Q K^T (both operands in shared memory) and
+//                   O += P V (P in tensor memory), tile A and B in turn, so that one
+//                   tile's softmax runs under the other's MMAs.
+//   warp 9          finds the CTA's next block, one ahead.
 //   warp 10         one lane issues the tensor-map copies: Q, and K and V tiles through a
 //                   ring of stages.
-//   warp 11         finds the CTA's next block, one ahead.
 // Tensor memory: S/P of A and B (128 columns each), O of A and B (128 each): all 512.
 //
 // The maximum that the probabilities are relative to may lag behind the true one by 2^11:
@@ -34,22 +34,21 @@
 //
 // Rows behind a sequence's end share its last tiles.  As query rows they are computed and
 // not stored; as keys they are masked by causality; as values they would meet
-// probability 0, and a NaN there would spread, so the MMA warps overwrite them with zeros first.
+// probability 0, and a NaN there would spread, so the MMA warp overwrites them with zeros first.
 //
-// Measured (two prompts of 16384 and 8200 tokens, 32 query heads on 8): 2.06 ms, 1.33
-// PFLOP/s of causal work, 0.71 of the measured bf16 peak; eight ragged prompts of up to 4113
-// tokens with 32 KV heads: 0.53 ms, 0.52 of it; 128 prompts of up to 512 tokens: 78 us.  What bounds it: the
-// tensor pipe is active for 58% of the cycles.  Per pass, a tile's softmax (about 1900 to 2200
-// cycles with the other tile's on the same schedulers) and its P.V and next scores (about
-// 1300, of which 768 are MMAs and the rest waits on barriers) come one after the other, and the
-// two tiles overlap only in part.  With an eighth of the MMAs it takes 0.69 of the time,
-// without the copies 0.97.  Tried and slower on the long prompts: two threads a row in 16
-// softmax warps (1.26x); tiles of 80 keys with P in columns of its own, so that the next
-// scores go out before P.V (1.07x and 1.22x); turns on the exponential unit (1.09x);
-// probabilities handed over once a pass (1.08x); one MMA warp for both tiles (1.03x); MMAs
-// issued by a softmax warp (1.5x: it stands still until they are taken).
-// Short prompts are bound by the length of one block's chain: copies, scores, softmax, P.V and output,
-// about 6500 cycles where all keys fit one tile.
+// Measured (two prompts of 16384 and 8200 tokens, 32 query heads on 8): 1.95 ms, 1.41
+// PFLOP/s of causal work, 0.75 of the measured bf16 peak; eight ragged prompts of up to
+// 4113 tokens with 32 KV heads: 0.47 ms, 0.60 of it; 128 prompts of up to 512 tokens: 69 us.
+// What bounds it: per pass, a tile's softmax (about 1300 cycles, of which the exponential
+// unit needs 512) and its P.V and next scores (1024 of MMAs and about 400 of waits for
+// barriers) come one after the other, and the two tiles overlap only in part.  Tried and
+// slower on the long prompts: probabilities handed over in halves (1.05x), the maximum checked
+// beside the exponentials instead of before them (1.08x), two threads a row in 16 softmax
+// warps (1.3x), tiles of 80 keys with P in columns of its own, so that the next scores go out
+// before P.V (1.13x), turns on the exponential unit (1.15x), MMAs issued by a softmax warp
+// (1.6x: it stands still until they are taken).  An MMA warp for each tile is level there and
+// 10% slower on short prompts.  Short prompts are bound by the length of one block's chain:
+// copies, scores, softmax, P.V and output.
 //
 // Every wait is bounded: one that runs out (a copy that never completes) ends all roles
 // of the CTA; the rows of its block are NaN, those of its later blocks not written.
@@ -69,7 +68,7 @@ namespace {
 
 constexpr int kRows = 128;                  // query rows of a tile, keys of a tile
 constexpr int kThreads = 384;               // three warpgroups
-constexpr int kMmaWarp = 8, kLoadWarp = 10;  // two MMA warps, one a tile
+constexpr int kMmaWarp = 8, kBlockWarp = 9, kLoadWarp = 10;
 // Registers a thread: the CTA's share at launch, and how the warpgroups split it (a
 // softmax thread holds a row of 128 scores).
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
@@ -79,7 +78,7 @@ constexpr int kHalfBytes = kTileBytes / 2;  // 128 rows of 128 bytes, 128-byte s
 constexpr int kStages = 4;                  // K and V tiles in flight
 constexpr int kMaxPack = 16;
 constexpr float kLag = 11.f;                // log2 by which the reference maximum may lag
-constexpr float kShift = 4.f;              // log2 of the probabilities' scale
+constexpr float kShift = 4.f;               // log2 of the probabilities' scale
 constexpr float kFar = 1 << 16;             // |log2 score| from which an offset in fp32 (2^-8 there) is not enough
 constexpr float kLog2eP = 1.4426950408889634f;
 constexpr int kPolls = 1 << 22;             // of a wait, each suspended by the hardware for a while
@@ -100,11 +99,10 @@ struct __align__(16) Bars {
   uint64_t q[2];            // Q tile landed
   uint64_t q_free[2];       // the block's last scores of it are done
   uint64_t full[kStages];   // K or V tile landed
-  uint64_t empty[kStages];  // both tiles are through with it
+  uint64_t empty[kStages];  // the MMAs that read it are done
   uint64_t s[2];            // scores of a tile written
-  uint64_t p[2][2];         // the probabilities of its first, its second 64 keys written
-  uint64_t o[2][2];         // their P.V done
-  uint64_t zeroed;          // value rows behind the sequence overwritten, for tile A
+  uint64_t p[2];            // its probabilities written
+  uint64_t o[2];            // their P.V done
   uint64_t block[2];        // block k written to slot k % 2
   uint64_t block_read[2];   // by every warp that works on it
   Block slot[2];
@@ -312,46 +310,17 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r) {
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
-  asm volatile("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
-  asm volatile("max.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
-}
-// A pair of fp32 registers: x c + b, and a sum.
-__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm volatile("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpair(uint64_t v, uint32_t &lo, uint32_t &hi) {
-  asm volatile("mov.b64 {%0, %1}, %2;\n" : "=r"(lo), "=r"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t c, uint64_t b) {
-  uint64_t r;
-  asm volatile("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(x), "l"(c), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm volatile("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm volatile("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t half2_of(uint32_t lo, uint32_t hi) {
-  uint32_t r;
-  asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(__uint_as_float(hi)), "f"(__uint_as_float(lo)));
-  return r;
 }
 
 // ---------------------------------------------------------------------------- blocks
-constexpr int kReaders = 11;  // warps that work on a block
+constexpr int kReaders = 10;  // warps that work on a block
 
 // Block k of this CTA into slot k % 2, for the warps that work on it.  The list is dealt out
 // back and forth, so that the first CTAs do not get the longer block of every round.
@@ -452,64 +421,60 @@ __device__ __forceinline__ void zero_rows(unsigned char *v, int tail, int lane) 
 }
 
 // -------------------------------------------------------------------------- products
-// Of tile x.  Scores and output of one tile take turns in its warp; the other tile's warp
-// keeps the tensor cores busy meanwhile.
-__device__ __forceinline__ void mma_role(const Cta &cta, Bars &sh, int x, int lane) {
+// Tile A and B in turn: a tile's P.V and its next scores go out together, and run while the
+// other tile's softmax does.
+__device__ __forceinline__ void mma_role(const Cta &cta, Bars &sh, int lane) {
   const uint32_t one = elect_one();
-  const uint32_t q0 = desc_lo(cta.sQ + x * kTileBytes, 16), k0 = desc_lo(cta.sKV, 16), v0 = desc_lo(cta.sKV, kHalfBytes);
-  const uint32_t tS = cta.tmem + x * kRows, tO = cta.tmem + 2 * kRows + x * kD;
+  const uint32_t q0 = desc_lo(cta.sQ, 16), k0 = desc_lo(cta.sKV, 16), v0 = desc_lo(cta.sKV, kHalfBytes);
   constexpr uint32_t kTile16 = kTileBytes >> 4;
   auto wait = [&](uint64_t *b, uint32_t parity) { return __all_sync(0xffffffffu, bar_wait(b, parity, &sh.abort)) != 0; };
   auto landed = [&](int c) { return wait(&sh.full[c % kStages], (c / kStages) & 1); };
   auto give = [&](int c) { tc_commit(&sh.empty[c % kStages], one); };
-  // Output of pass t of the tile with the V tile of copy c, keys 64 g .. 64 g + 63: the first half
-  // runs while the softmax works on the second.  The first pass of a block starts a new output,
-  // its probabilities coming after the softmax has read the last one.
-  auto pv = [&](int t, int c, int g, bool add) {
-    if (!wait(&sh.p[x][g], t & 1)) return false;
-    tc_fence_after();
-    mma_pv(tO, tS + 32 * g, v0 + (c % kStages) * kTile16 + 512 * g, kIdescPV, add, one);
-    tc_commit(&sh.o[x][g], one);
-    return true;
-  };
-  auto qk = [&](int c) {  // scores with the K tile of copy c
-    mma_qk(tS, q0, k0 + (c % kStages) * kTile16, kIdescQK, 0, one);
-    tc_commit(&sh.s[x], one);
-    give(c);
-  };
-  int c = 0, t = 0, tiles = 0, zeroed = 0;  // copies, passes, Q tiles and zeroed value tiles before
+  int c = 0, t[2] = {0, 0}, tiles[2] = {0, 0};  // copies, passes and Q tiles before
   Block w;
+  auto qk = [&](int x, int c) {  // scores of tile x with the K tile of copy c
+    mma_qk(cta.tmem + x * kRows, q0 + x * kTile16, k0 + (c % kStages) * kTile16, kIdescQK, 0, one);
+    tc_commit(&sh.s[x], one);
+  };
   for (int k = 0; next_block(sh, k, lane, &w); ++k) {
-    const int nt = x ? w.nt1 : w.nt0;
-    for (int i = 0; i < 2 * (w.n - nt); ++i, ++c) {  // passes that are the other tile's alone
-      if (!landed(c)) return;
-      if (one) bar_arrive(&sh.empty[c % kStages]);
-    }
-    if (nt == 0) continue;
-    if (!wait(&sh.q[x], tiles & 1) || !landed(c)) return;
-    ++tiles;
-    tc_fence_after();
-    qk(c);
-    for (int i = 0; i < nt; ++i, ++t, c += 2) {
-      const bool more = i + 1 < nt;
-      if (!more) tc_commit(&sh.q_free[x], one);
-      if (!landed(c + 1)) return;
-      if (i == 0 && nt == w.n && w.tail < kRows) {
-        // value rows behind the sequence: B's warp clears them for both tiles
-        const bool shared = w.nt0 == w.nt1;
-        if (x == 1 || !shared)
-          zero_rows(cta.tiles + (2 + (c + 1) % kStages) * kTileBytes, w.tail, lane);
-        else if (!wait(&sh.zeroed, zeroed & 1))
-          return;
-        if (x == 1 && shared && lane == 0) bar_arrive(&sh.zeroed);
-        zeroed += shared;
+    if (!landed(c)) return;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      if (!(x ? w.nt1 : w.nt0)) continue;
+      if (!wait(&sh.q[x], tiles[x] & 1)) return;
+      ++tiles[x];
+      tc_fence_after();
+      if ((x ? w.nt1 : w.nt0) == w.n) {
+        qk(x, c);
+        if (w.n == 1) tc_commit(&sh.q_free[x], one);
       }
-      if (!pv(t, c + 1, 0, i > 0)) return;
-      if (more && !landed(c + 2)) return;
-      if (!pv(t, c + 1, 1, true)) return;
+    }
+    give(c);
+    if (!landed(c + 1)) return;
+    if (w.tail < kRows) zero_rows(cta.tiles + (2 + (c + 1) % kStages) * kTileBytes, w.tail, lane);
+    for (int i = 0; i < w.n; ++i, c += 2) {
+      const int left = w.n - 1 - i;  // key tile of this pass
+      if (i && !landed(c + 1)) return;
+      if (left && !landed(c + 2)) return;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int nt = x ? w.nt1 : w.nt0;
+        if (left < nt) {
+          if (!wait(&sh.p[x], t[x] & 1)) return;
+          tc_fence_after();
+          const uint32_t d = cta.tmem + 2 * kRows + x * kD, a = cta.tmem + x * kRows, v = v0 + ((c + 1) % kStages) * kTile16;
+          mma_pv(d, a, v, kIdescPV, left < nt - 1, one);
+          mma_pv(d, a + 32, v + 512, kIdescPV, 1, one);
+          tc_commit(&sh.o[x], one);
+          ++t[x];
+        }
+        if (left && left - 1 < nt) {
+          qk(x, c + 2);
+          if (left == 1) tc_commit(&sh.q_free[x], one);
+        }
+      }
       give(c + 1);
-      // the scores go where the probabilities were: MMAs run in the order of issue
-      if (more) qk(c + 2);
+      if (left) give(c + 2);
     }
   }
 }
@@ -535,52 +500,15 @@ __device__ __forceinline__ float max64(const uint32_t *s) {
   return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
 }
 
-// Probabilities 2^(c0 s + b) of 32 scores, as fp16 pairs in p, added to the two sums in l;
-// the largest exponent goes into mx.  s is used up.  In batches of 8, the sums and
-// conversions of a batch behind the exponentials of the next one.
-__device__ __forceinline__ void exp32(uint32_t *s, uint32_t *p, uint64_t c2, uint64_t b2, uint64_t *l, float *mx) {
-#pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const uint64_t e = fma2(pair(s[2 * k], s[2 * k + 1]), c2, b2);
-    unpair(e, s[2 * k], s[2 * k + 1]);
-  }
-  auto finish = [&](int j) {  // sums and conversions of batch j
-#pragma unroll
-    for (int i = 4 * j; i < 4 * j + 4; ++i) {
-      l[i & 1] = add2(l[i & 1], pair(s[2 * i], s[2 * i + 1]));
-      p[i] = half2_of(s[2 * i], s[2 * i + 1]);
-    }
-  };
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      mx[i] = max3(mx[i], __uint_as_float(s[8 * j + 2 * i]), __uint_as_float(s[8 * j + 2 * i + 1]));
-#pragma unroll
-    for (int i = 8 * j; i < 8 * j + 8; ++i) s[i] = __float_as_uint(ex2(__uint_as_float(s[i])));
-    if (j) finish(j - 1);
-  }
-  finish(3);
-}
-
 __device__ __forceinline__ void softmax_role(const PackedAttentionArgs &a, const Cta &cta, Bars &sh, int x, int warp,
                                              int lane) {
   const int r = 32 * warp + lane;  // row of tile x
   const uint32_t lanes = (uint32_t)(32 * warp) << 16;
   const uint32_t tS = cta.tmem + x * kRows + lanes, tO = cta.tmem + 2 * kRows + x * kD + lanes;
   const float c0 = a.softmax_scale * kLog2eP;
-  const uint64_t c2 = pair(__float_as_uint(c0), __float_as_uint(c0));
   // whole 32-byte sectors where the output's rows allow it
   const bool wide = ((reinterpret_cast<uintptr_t>(a.out.p) | (uintptr_t)(a.out.ts * 2) | (uintptr_t)(a.out.hs * 2)) & 31) == 0;
   auto wait = [&](uint64_t *b, uint32_t parity) { return __all_sync(0xffffffffu, bar_wait(b, parity, &sh.abort)) != 0; };
-  // the probabilities of keys 64 g .. 64 g + 63 go over the first half of the scores, read by then
-  auto put = [&](int g, const uint32_t *p) {
-    tmem_st32(tS + 32 * g, p);
-    tc_wait_st();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) bar_arrive(&sh.p[x][g]);
-  };
   bool ok = true;
   int t0 = 0;  // passes of this tile in the blocks before
   Block w;
@@ -588,97 +516,79 @@ __device__ __forceinline__ void softmax_role(const PackedAttentionArgs &a, const
     const int base = x ? w.base1 : w.base0, nt = x ? w.nt1 : w.nt0;
     if (nt == 0) continue;
     const int token = base + r % cta.tpt;
-    float m = 0.f;           // the reference maximum
-    uint64_t l[2] = {0, 0};  // the sum, in four parts
-    uint64_t b2 = 0;         // the exponents' offset with this maximum, twice
-    // Far from zero the offset's rounding would count: there the maximum is subtracted first.
-    bool far = false;
-    auto refer = [&](float mx) {
-      m = mx;
-      far = __any_sync(0xffffffffu, fabsf(m * c0) > kFar);
-      const uint32_t b = __float_as_uint(far ? kShift : kShift - m * c0);
-      b2 = pair(b, b);
-    };
+    float m = 0.f, off = 0.f;  // the reference maximum, and the exponents' offset with it
+    float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;  // the sum, in four parts
+    bool far = false;          // far from zero that offset has no digits: subtract the maximum first
     const int last = token - (nt - 1) * kRows;  // the row's own key in the tile on the diagonal
-    // 64 keys at a time, one body for all of them: code that is read once a block costs more
-    // than it runs
-    for (int q = 2 * t0; q < 2 * (t0 + nt) && ok; ++q) {
-      const int g = q & 1, t = q >> 1;
-      if (g == 0) {
-        ok = wait(&sh.s[x], t & 1);
-        if (!ok) break;
-        tc_fence_after();
-      }
-      const bool diagonal = t == t0;
-      bool fresh = q == 2 * t0;  // the maximum has to be found before the exponentials
-      uint32_t p[32];
-      if (g == 1 && diagonal && __all_sync(0xffffffffu, last < 64)) {  // no row sees these keys
+    for (int t = t0; t < t0 + nt && ok; ++t) {
+      ok = wait(&sh.s[x], t & 1);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t s[kRows];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) p[j] = 0;
-        put(g, p);
-        continue;
-      }
-      const bool cut = diagonal && __any_sync(0xffffffffu, last < 64 * g + 63);
-      for (;;) {
-        uint32_t s[64];
-        tmem_ld32(tS + 64 * g, s);
-        tmem_ld32(tS + 64 * g + 32, s + 32);
-        tc_wait_ld();
-        landed32(s);
-        landed32(s + 32);
-        if (cut) {
+      for (int j = 0; j < 4; ++j) tmem_ld32(tS + 32 * j, s + 32 * j);
+      tc_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 64; ++j)
-            if (j + 64 * g > last) s[j] = 0xff800000u;
-        }
-        if (fresh) {
-          float mn = max64(s);
-          if (q != 2 * t0) {
-            mn = fmaxf(m, mn);
-            const float al = ex2((m - mn) * c0);
-            const uint64_t al2 = pair(__float_as_uint(al), __float_as_uint(al));
-            l[0] = mul2(l[0], al2);
-            l[1] = mul2(l[1], al2);
-            ok = wait(&sh.o[x][g ^ 1], (t - 1 + g) & 1);  // the last product into the output
-            if (!ok) break;
-            tc_fence_after();
+      for (int j = 0; j < 4; ++j) landed32(s + 32 * j);
+      if (t == t0) {  // the tile on the diagonal
+#pragma unroll
+        for (int j = 0; j < kRows; ++j)
+          if (j > last) s[j] = 0xff800000u;
+      }
+      const float mx = fmaxf(max64(s), max64(s + 64));
+      const bool first = t == t0;
+      if (first || __any_sync(0xffffffffu, (mx - m) * c0 > kLag)) {  // a new reference
+        const float mn = first ? mx : fmaxf(m, mx);
+        if (!first) {
+          const float al = ex2((m - mn) * c0);
+          sum0 = __fmul2_rn(sum0, make_float2(al, al));
+          sum1 = __fmul2_rn(sum1, make_float2(al, al));
+          ok = wait(&sh.o[x], (t - 1) & 1);  // the last product into the output
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll 1
-            for (int j = 0; j < 4; ++j) {
-              uint32_t o[32];
-              tmem_ld32(tO + 32 * j, o);
-              tc_wait_ld();
-              landed32(o);
+          for (int j = 0; j < 4; ++j) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32 * j, o);
+            tc_wait_ld();
+            landed32(o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-              tmem_st32(tO + 32 * j, o);
-            }
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+            tmem_st32(tO + 32 * j, o);
           }
-          refer(mn);
         }
-        if (far) {
-#pragma unroll
-          for (int j = 0; j < 64; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) - m);
-        }
-        // With the maximum of before, which nearly always still serves: whether it does is
-        // found beside the exponentials instead of before them.
-        const uint64_t l0 = l[0], l1 = l[1];
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        exp32(s, p, c2, b2, l, mx);
-        exp32(s + 32, p + 16, c2, b2, l, mx);
-        if (fresh || !__any_sync(0xffffffffu, fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) > kShift + kLag)) break;
-        l[0] = l0;
-        l[1] = l1;
-        fresh = true;
+        m = mn;
+        far = __any_sync(0xffffffffu, fabsf(m * c0) > kFar);
+        off = far ? kShift : kShift - m * c0;
       }
-      if (ok) put(g, p);
+      if (__builtin_expect(far, 0)) {
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) - m);
+      }
+      const float2 c2 = make_float2(c0, c0), b2 = make_float2(off, off);
+#pragma unroll
+      for (int j = 0; j < kRows / 2; ++j) {
+        const float2 e = __ffma2_rn(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, b2);
+        const float2 v = make_float2(ex2(e.x), ex2(e.y));
+        if (j & 1)
+          sum1 = __fadd2_rn(sum1, v);
+        else
+          sum0 = __fadd2_rn(sum0, v);
+        s[j] = h22u(__floats2half2_rn(v.x, v.y));
+      }
+      tmem_st32(tS, s);
+      tmem_st32(tS + 32, s + 32);
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&sh.p[x]);
     }
     t0 += nt;
-    ok = ok && wait(&sh.o[x][0], (t0 - 1) & 1) && wait(&sh.o[x][1], (t0 - 1) & 1);
+    ok = ok && wait(&sh.o[x], (t0 - 1) & 1);
     tc_fence_after();
     // ---- the tile's rows
-    uint32_t l_lo, l_hi;
-    unpair(add2(l[0], l[1]), l_lo, l_hi);
-    const float inv = ok ? 1.f / (__uint_as_float(l_lo) + __uint_as_float(l_hi)) : __int_as_float(0x7fc00000);
+    const float2 sum = __fadd2_rn(sum0, sum1);
+    const float inv = ok ? 1.f / (sum.x + sum.y) : __int_as_float(0x7fc00000);
     uint16_t *dst = a.out.p + (int64_t)(w.start + token) * a.out.ts + (int64_t)(w.head0 + r / cta.tpt) * a.out.hs;
     const bool mine = token < w.len;
 #pragma unroll 1
@@ -691,7 +601,7 @@ __device__ __forceinline__ void softmax_role(const PackedAttentionArgs &a, const
       landed32(o + 32);
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        o[i] = half2_of(__float_as_uint(__uint_as_float(o[2 * i]) * inv), __float_as_uint(__uint_as_float(o[2 * i + 1]) * inv));
+        o[i] = h22u(__floats2half2_rn(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv));
       if (mine) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -733,16 +643,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_init(&sh.q[x], 1);
         bar_init(&sh.q_free[x], 1);
         bar_init(&sh.s[x], 1);
-        for (int g = 0; g < 2; ++g) {
-          bar_init(&sh.p[x][g], 4);
-          bar_init(&sh.o[x][g], 1);
-        }
+        bar_init(&sh.p[x], 4);
+        bar_init(&sh.o[x], 1);
       }
       for (int i = 0; i < kStages; ++i) {
         bar_init(&sh.full[i], 1);
-        bar_init(&sh.empty[i], 2);
+        bar_init(&sh.empty[i], 1);
       }
-      bar_init(&sh.zeroed, 1);
       for (int i = 0; i < 2; ++i) {
         bar_init(&sh.block[i], 1);
         bar_init(&sh.block_read[i], kReaders);
@@ -766,9 +673,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
     if (warp == kLoadWarp)
       load_role(maps, cta, sh, lane);
-    else if (warp < kLoadWarp)
-      mma_role(cta, sh, warp - kMmaWarp, lane);
-    else
+    else if (warp == kMmaWarp)
+      mma_role(cta, sh, lane);
+    else if (warp == kBlockWarp)
       block_role(cta, sh, lane);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
