@@ -224,6 +224,21 @@ def test_attention_offsets_past_32_bits():
     check_attention(o, q, k, v, cu, 0.1)
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(25, 25), (50, 25), (24, 24), (96, 24)])
+def test_attention_head_sets(Hq, Hkv):
+    """A token axis so long that the heads are taken in sets (K and V past the L2 cache), of even and uneven
+    sizes: the same bits as the same sequences at the start of a short axis."""
+    T, lens = 20000, [2100, 0, 900, 33]
+    x = torch.randn((T, Hq + 2 * Hkv, D), device="cuda", generator=torch.Generator("cuda").manual_seed(17),
+                    dtype=torch.float32).to(torch.float16)
+    cu = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32, device="cuda")
+    n = sum(lens)
+    out = [kivi.kivi_prefill_attention_packed(t[:, :Hq], t[:, Hq:Hq + Hkv], t[:, Hq + Hkv:], cu, 0.1)
+           for t in (x, x[:n])]
+    assert torch.equal(out[0][:n], out[1]) and (out[0][n:] == 0).all()
+    check_attention(out[0], x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], cu, 0.1, seqs=[0, 3], heads=[0, Hq // 2, Hq - 1])
+
+
 def test_attention_bounds_that_make_no_sense():
     """Bounds outside the axis are clamped; falling ones are empty sequences."""
     (q, k, v), _ = pack([200], [2, 1, 1], "tokens", 9)
