@@ -289,19 +289,15 @@ def _plain_attention(s):
     R = q.shape[1] // k.shape[1]
     cu = s["cu"].tolist()
     for a, b in zip(cu[:-1], cu[1:]):
-        n = b - a
-        if n == 0:
-            continue
-        later = torch.ones((n, n), dtype=torch.bool, device=q.device).triu(1)
-        step = max(1, 2**30 // (R * n * n))  # KV heads at once: 4 GB of scores
-        for h in range(0, k.shape[1], step):
-            ks, vs = (x[a:b, h:h + step].float().transpose(0, 1) for x in (k, v))
-            qs = q[a:b, h * R:(h + ks.shape[0]) * R].float().transpose(0, 1).reshape(ks.shape[0], R * n, D)
-            x = torch.bmm(qs, ks.transpose(1, 2)).mul_(s["scale"]).view(-1, R, n, n)
+        later = torch.ones((b - a, b - a), dtype=torch.bool, device=q.device).triu(1)
+        for h in range(k.shape[1]):
+            qs = q[a:b, h * R:(h + 1) * R].float().transpose(0, 1)
+            x = (qs @ k[a:b, h].float().t()).mul_(s["scale"])
             x.masked_fill_(later, -math.inf)
-            x.sub_(x.amax(-1, keepdim=True)).exp_()
-            o = torch.bmm(x.view(-1, R * n, n), vs).view(-1, R, n, D) / x.sum(-1, keepdim=True)
-            out[a:b, h * R:(h + ks.shape[0]) * R] = o.reshape(-1, n, D).transpose(0, 1).to(torch.float16)
+            if b > a:
+                x.sub_(x.amax(-1, keepdim=True)).exp_()
+            o = (x @ v[a:b, h].float()) / x.sum(-1, keepdim=True)
+            out[a:b, h * R:(h + 1) * R] = o.transpose(0, 1).to(torch.float16)
     return out
 
 
