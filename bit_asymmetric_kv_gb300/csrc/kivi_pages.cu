@@ -100,7 +100,9 @@ __device__ int block_scan(int v, Shared &sh, int *total) {
 }
 
 // Gives every CTA the counts of all (two of them at once): the sums over the CTAs
-// before this one, and over all.
+// before this one, and over all.  It writes into the other CTAs' shared memory, so a cluster
+// barrier has to come before it: until then one of them may not have started.  A kernel that
+// has none by then arrives at one on entry and waits for it here, behind its counting pass.
 struct Spread {
   int before, all;
 };
@@ -194,6 +196,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   __shared__ Shared sh;
   __shared__ int s_rank[64];  // missing entries of this CTA's rows, then the rank of each row's first
   cg::cluster_group cl = cg::this_cluster();
+  cl.barrier_arrive();  // this CTA runs: see exchange()
   const int r = (int)cl.block_rank(), lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int per = (a.B + kPoolCtas - 1) / kPoolCtas;  // <= 64
   const int b0 = min(a.B, per * r), rows = min(a.B, b0 + per) - b0;
@@ -220,6 +223,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   int missing;
   const int before = block_scan((int)threadIdx.x < rows ? s_rank[threadIdx.x] : 0, sh, &missing);
   Spread fr, ms;
+  cl.barrier_wait();  // every CTA runs
   exchange(cl, sh, nfree, missing, &fr, &ms);
   if ((int)threadIdx.x < rows) s_rank[threadIdx.x] = ms.before + before;
   const int got = min(fr.all, ms.all);
@@ -436,11 +440,13 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   __shared__ Shared sh;
   cg::cluster_group cl = cg::this_cluster();
+  cl.barrier_arrive();  // this CTA runs: see exchange()
   const int r = (int)cl.block_rank();
   int lo, hi;
   slice(r, a.num_pages, &lo, &hi);
   Spread live, movers, holes, unused;
   const int nlive = count_slice(a.refs, lo, hi, 0, sh, [](int c, int) { return c > 0; });
+  cl.barrier_wait();  // every CTA runs
   exchange(cl, sh, nlive, 0, &live, &unused);
   const int L = live.all;
   auto moves = [L](int c, int id) { return c > 0 && id >= L; };
