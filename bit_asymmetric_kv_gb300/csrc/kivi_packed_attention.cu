@@ -33,8 +33,10 @@
 // and their rounding, 2^-11 of each, is the only one below fp32 before the output's.
 //
 // Rows behind a sequence's end share its last tiles.  As query rows they are computed and
-// not stored; as keys they are masked by causality; as values they would meet
-// probability 0, and a NaN there would spread, so the MMA warp overwrites them with zeros first.
+// not stored, and have no vote in what a warp does for its rows together (a new reference,
+// the form for scores far from zero), so that a prompt's bits are those that it has alone;
+// as keys they are masked by causality; as values they would meet probability 0, and a NaN
+// there would spread, so the MMA warp overwrites them with zeros first.
 //
 // Measured (two prompts of 16384 and 8200 tokens, 32 query heads on 8): 1.95 ms, 1.41
 // PFLOP/s of causal work, 0.75 of the measured bf16 peak; eight ragged prompts of up to
@@ -542,6 +544,7 @@ __device__ __forceinline__ void softmax_role(const PackedAttentionArgs &a, const
     float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;  // the sum, in four parts
     bool far = false;          // far from zero that offset has no digits: subtract the maximum first
     const int last = token - (nt - 1) * kRows;  // the row's own key in the tile on the diagonal
+    const bool mine = token < w.len;            // the sequence's own row
     for (int t = t0; t < t0 + nt && ok; ++t) {
       ok = wait(&sh.s[x], t & 1);
       if (!ok) break;
@@ -559,7 +562,7 @@ __device__ __forceinline__ void softmax_role(const PackedAttentionArgs &a, const
       }
       const float mx = fmaxf(max64(s), max64(s + 64));
       const bool first = t == t0;
-      if (first || __any_sync(0xffffffffu, (mx - m) * c0 > kLag)) {  // a new reference
+      if (first || __any_sync(0xffffffffu, mine && (mx - m) * c0 > kLag)) {  // a new reference
         const float mn = first ? mx : fmaxf(m, mx);
         if (!first) {
           const float al = ex2((m - mn) * c0);
@@ -580,7 +583,7 @@ __device__ __forceinline__ void softmax_role(const PackedAttentionArgs &a, const
           }
         }
         m = mn;
-        far = __any_sync(0xffffffffu, fabsf(m * c0) > kFar);
+        far = __any_sync(0xffffffffu, mine && fabsf(m * c0) > kFar);
         off = far ? kShift : kShift - m * c0;
       }
       if (__builtin_expect(far, 0)) {
@@ -612,7 +615,6 @@ __device__ __forceinline__ void softmax_role(const PackedAttentionArgs &a, const
     const float2 sum = __fadd2_rn(sum0, sum1);
     const float inv = ok ? 1.f / (sum.x + sum.y) : __int_as_float(0x7fc00000);
     uint16_t *dst = a.out.p + (int64_t)(w.start + token) * a.out.ts + (int64_t)(w.head0 + r / cta.tpt) * a.out.hs;
-    const bool mine = token < w.len;
 #pragma unroll 1
     for (int j = 0; j < 2; ++j) {
       uint32_t o[64];

@@ -413,7 +413,8 @@ typedef struct {
  * The rows of a sequence must be finite; softmax_scale must be positive and at most 2^127
  * (KIVI_ERR_ARG).  out's elements must not overlap one another (KIVI_ERR_ARG) or the
  * inputs.  Scores, running maximum and sum, and the output's accumulators are fp32;
- * the probabilities enter the P.V product in fp16.  n_tokens == 0 launches nothing.
+ * the probabilities enter the P.V product in fp16.  A sequence's outputs are the same bits
+ * whatever stands before and behind it.  n_tokens == 0 launches nothing.
  * Nothing is allocated.  The first call on a device asks the CUDA runtime about the kernel
  * (its registers, the device's SMs, the tensor-map encoder) and remembers the answer: make it
  * before capturing calls in a CUDA graph.  Device faults: every wait of the kernel is
