@@ -564,8 +564,13 @@ __device__ __forceinline__ void softmax_role(const PackedAttentionArgs &a, const
       const bool first = t == t0;
       if (first || __any_sync(0xffffffffu, mine && (mx - m) * c0 > kLag)) {  // a new reference
         const float mn = first ? mx : fmaxf(m, mx);
+        const bool far_now = __any_sync(0xffffffffu, mine && fabsf(mn * c0) > kFar);
+        const float off_now = far_now ? kShift : kShift - mn * c0;
         if (!first) {
-          const float al = ex2((m - mn) * c0);
+          // What lies between the weights before, 2^(c0 (s - [far] m) + off), and those from now on.
+          // It takes both offsets as they were rounded (by up to 2^-9 below kFar): from the maxima
+          // alone old and new weights would be as far apart as the two roundings, 0.27% at most.
+          const float al = ex2(fmaf((far ? m : 0.f) - (far_now ? mn : 0.f), c0, off_now - off));
           sum0 = __fmul2_rn(sum0, make_float2(al, al));
           sum1 = __fmul2_rn(sum1, make_float2(al, al));
           ok = wait(&sh.o[x], (t - 1) & 1);  // the last product into the output
@@ -583,8 +588,8 @@ __device__ __forceinline__ void softmax_role(const PackedAttentionArgs &a, const
           }
         }
         m = mn;
-        far = __any_sync(0xffffffffu, mine && fabsf(m * c0) > kFar);
-        off = far ? kShift : kShift - m * c0;
+        far = far_now;
+        off = off_now;
       }
       if (__builtin_expect(far, 0)) {
 #pragma unroll

@@ -1,4 +1,16 @@
-"""Packed attention row by row on the GPU: what a row's result may depend on."""
+"""Packed attention row by row on the GPU: what a row's result may depend on, and how its
+weights hold together over the whole range of scores.
+
+Tolerance of the weights' test, before any run.  The scores are integers that fp32 holds exactly, at
+most 9 apart, and every |v| is 1, so that sum_j p_j |v_j| / l = 1:
+  - the output is rounded to fp16 once: 2^-11 |out| + 2^-25;
+  - the probabilities enter the P.V product in fp16 (none is subnormal there): 2^-11;
+  - an exponent is a difference of at most 9 log2(e) + 4 = 17 and a rescale's one of 13; scale and
+    log2(e) are rounded to fp32 (2 * 2^-24 of the difference), the result once (2^-24 of it), an
+    exponential is 2^-22 off: less than 2^-18 of a weight in all, numerator and denominator: 2^-17;
+  - the sums over the keys in fp32: 2^-22 per step of 16 keys.
+Nothing in it grows with the scores themselves.
+"""
 from __future__ import annotations
 
 import math
@@ -45,3 +57,33 @@ def test_bits_do_not_depend_on_what_stands_behind(Hq, Hkv, n, behind, as_prompt)
     cu = cu_of(0, n, n + 200) if as_prompt else cu_of(0, n)
     got = kivi.kivi_prefill_attention_packed(q, k, v, cu, 0.1)
     assert torch.equal(got[:n], alone)
+
+
+# of each head: scores 256 k0 + a, and 9 more for the first key, whose tile comes last
+SCORES = {
+    "near": [(177, 24), (174, 10), (172, 31), (169, 17)],             # log2 just below 2^16
+    "crossing-up": [(177, 107), (177, 109), (177, 110), (177, 112)],  # from below 2^16 to above
+    "crossing-down": [(-178, 133), (-178, 136), (-178, 138), (-178, 141)],
+    "beyond": [(250, 100), (500, 3), (-400, 5), (1000, 7)],
+    "small": [(0, 0), (1, 3), (-2, 7), (40, 1)],
+}
+
+
+@pytest.mark.parametrize("kind", list(SCORES))
+def test_weights_before_and_after_a_new_maximum_agree(kind):
+    """Thousands of equal weights against one that is e^9 times as large and met last: the two sides' sums are
+    alike, so that a mismatch between the weights before and after the jump shows."""
+    n, heads = 8300, SCORES[kind]
+    q = torch.zeros((n, len(heads), D), dtype=torch.float16, device="cuda")
+    k, v = torch.zeros_like(q), torch.ones_like(q)
+    q[:, :, 0], q[:, :, 1] = 256.0, 1.0
+    for h, (k0, a) in enumerate(heads):
+        k[:, h, 0], k[:, h, 1] = k0, a
+        k[0, h, 1] = a + 9
+    v[0] = -1.0
+    out = kivi.kivi_prefill_attention_packed(q, k, v, cu_of(0, n), 1.0)
+    i = torch.arange(n, dtype=torch.float64, device="cuda")[:, None, None]
+    ref = (i - math.exp(9.0)) / (i + math.exp(9.0))
+    tol = 2.0**-11 * ref.abs() + 2.0**-25 + 2.0**-11 + 2.0**-17 + (n / 16) * 2.0**-22
+    worst = ((out.double() - ref).abs() - tol).amax((0, 2)).tolist()
+    assert max(worst) <= 0, worst
