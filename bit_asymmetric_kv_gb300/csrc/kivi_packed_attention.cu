@@ -749,6 +749,11 @@ bool encode(CUtensorMap *m, const PackedRows &r, int T, int heads, int box_token
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_all(Maps *m, const PackedAttentionArgs &a, int pack) {
+  return encode(&m->q, a.q, a.T, a.Hq, kRows / pack, pack) && encode(&m->k, a.k, a.T, a.Hkv, kRows, 1) &&
+         encode(&m->v, a.v, a.T, a.Hkv, kRows, 1);
+}
+
 int pack_of(const PackedAttentionArgs &a) {
   const int R = a.Hq / a.Hkv;
   int p = 1;
@@ -773,13 +778,13 @@ int64_t blocks_of(const PackedAttentionArgs &a) {
   return ((int64_t)a.T / (2 * kRows / pack) + a.n_seqs) * (a.Hq / pack);
 }
 
-// SMs of the current device.  Once per device: the shared memory's limit, and that the kernel has
+// The current device and its SMs.  Once per device: the shared memory's limit, and that the kernel has
 // the registers that the warpgroups' split of them rests on.
-cudaError_t prepare_kernel(int *sms) {
+cudaError_t prepare_kernel(int *device, int *sms) {
   static std::atomic<int> known[64];  // SMs + 1 of a device that is ready, else 0
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  cudaError_t e = cudaGetDevice(device);
   if (e != cudaSuccess) return e;
+  const int dev = *device;
   const int n = dev < 64 ? known[dev].load(std::memory_order_acquire) : 0;
   if (n) {
     *sms = n - 1;
@@ -800,13 +805,17 @@ bool packed_attention_fits(const PackedAttentionArgs &a) { return blocks_of(a) <
 
 cudaError_t launch_packed_attention(const PackedAttentionArgs &a, cudaStream_t st) {
   const int pack = pack_of(a);
-  Maps maps;
-  if (!encode(&maps.q, a.q, a.T, a.Hq, kRows / pack, pack) || !encode(&maps.k, a.k, a.T, a.Hkv, kRows, 1) ||
-      !encode(&maps.v, a.v, a.T, a.Hkv, kRows, 1))
-    return cudaErrorInvalidValue;
-  int sms = 0;
-  cudaError_t e = prepare_kernel(&sms);
+  int dev = 0, sms = 0;
+  cudaError_t e = prepare_kernel(&dev, &sms);
   if (e != cudaSuccess) return e;
+  Maps maps;
+  if (!encode_all(&maps, a, pack)) {
+    // The encoder is a driver call and wants a context.  A host thread that has not called the
+    // runtime yet has none, and cudaSetDevice gives it the device's; any other thread keeps the
+    // context that it has, since the maps are made at once.
+    if ((e = cudaSetDevice(dev)) != cudaSuccess) return e;
+    if (!encode_all(&maps, a, pack)) return cudaErrorInvalidValue;
+  }
   packed_attention_kernel<<<(unsigned)std::min<int64_t>(blocks_of(a), sms), kThreads, kSmem, st>>>(a, maps, pack, sets_of(a, pack));
   return cudaGetLastError();
 }

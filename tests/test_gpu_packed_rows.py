@@ -1,5 +1,5 @@
-"""Packed attention row by row on the GPU: what a row's result may depend on, and how its
-weights hold together over the whole range of scores.
+"""Packed attention row by row on the GPU: what a row's result may depend on, how its weights hold
+together over the whole range of scores, and calls from other host threads.
 
 Tolerance of the weights' test, before any run.  The scores are integers that fp32 holds exactly, at
 most 9 apart, and every |v| is 1, so that sum_j p_j |v_j| / l = 1:
@@ -14,6 +14,7 @@ Nothing in it grows with the scores themselves.
 from __future__ import annotations
 
 import math
+import threading
 
 import pytest
 import torch
@@ -87,3 +88,23 @@ def test_weights_before_and_after_a_new_maximum_agree(kind):
     tol = 2.0**-11 * ref.abs() + 2.0**-25 + 2.0**-11 + 2.0**-17 + (n / 16) * 2.0**-22
     worst = ((out.double() - ref).abs() - tol).amax((0, 2)).tolist()
     assert max(worst) <= 0, worst
+
+
+def test_a_thread_that_has_called_nothing_yet():
+    """A host thread whose first CUDA call is this one."""
+    (q, k, v), cu = pack([100, 44], [4, 2, 2], "tokens", 50)
+    want = kivi.kivi_prefill_attention_packed(q, k, v, cu, 0.1)
+    out, stream, seen = torch.zeros_like(want), torch.cuda.current_stream().cuda_stream, []
+
+    def call():
+        try:
+            kivi.kivi_prefill_attention_packed(q, k, v, cu, 0.1, out=out, stream=stream)
+        except Exception as e:  # noqa: BLE001
+            seen.append(e)
+
+    t = threading.Thread(target=call)
+    t.start()
+    t.join()
+    assert not seen, seen
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
