@@ -1,5 +1,5 @@
 """Packed attention row by row on the GPU: what a row's result may depend on, how its weights hold
-together over the whole range of scores, and calls from other host threads.
+together over the whole range of scores, which rows clamped bounds give, and calls from other host threads.
 
 Tolerance of the weights' test, before any run.  The scores are integers that fp32 holds exactly, at
 most 9 apart, and every |v| is 1, so that sum_j p_j |v_j| / l = 1:
@@ -21,7 +21,7 @@ import torch
 
 from bit_asymmetric_kv_gb300 import build as kbuild
 from bit_asymmetric_kv_gb300 import kivi
-from test_gpu_packed_prefill import pack
+from test_gpu_packed_prefill import check_attention, pack
 
 pytestmark = pytest.mark.gpu
 D = 128
@@ -88,6 +88,33 @@ def test_weights_before_and_after_a_new_maximum_agree(kind):
     tol = 2.0**-11 * ref.abs() + 2.0**-25 + 2.0**-11 + 2.0**-17 + (n / 16) * 2.0**-22
     worst = ((out.double() - ref).abs() - tol).amax((0, 2)).tolist()
     assert max(worst) <= 0, worst
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(2, 1), (2, 2)])
+@pytest.mark.parametrize("bounds,seqs", [
+    ([-50, 90, 60, 2**31 - 1], [(0, 90), None, (60, 200)]),            # rows 60 .. 89 in two: not looked at
+    ([-2**31, 90, 90, 2**31 - 1], [(0, 90), None, (90, 200)]),
+    ([-50, -1, 90, 200], [None, (0, 90), (90, 200)]),
+    ([-3, 200, 200, 500], [(0, 200), None, None]),
+    ([200, 2**31 - 1, 300, 1000], [None, None, None]),                 # all past the axis
+    ([-9, -5, -5, 0], [None, None, None]),                             # all before it
+])
+def test_clamped_bounds(Hq, Hkv, bounds, seqs):
+    """Starts are clamped to the axis and ends to [start, axis]: every row of one sequence has the bits that the
+    sequence has alone, within the tolerance of the formula, and rows of none are left."""
+    (q, k, v), _ = pack([200], [Hq, Hkv, Hkv], "tokens", 9)
+    out = torch.full(q.shape, 3.0, dtype=torch.float16, device="cuda")
+    kivi.kivi_prefill_attention_packed(q, k, v, cu_of(*bounds), 0.1, out=out)
+    times = torch.zeros(200, dtype=torch.int32, device="cuda")
+    for a, b in filter(None, seqs):
+        times[a:b] += 1
+    for a, b in filter(None, seqs):
+        Q, K, V, cu = q[a:b], k[a:b], v[a:b], cu_of(0, b - a)
+        alone = kivi.kivi_prefill_attention_packed(Q, K, V, cu, 0.1)
+        check_attention(alone, Q, K, V, cu, 0.1)
+        only = times[a:b] == 1
+        assert only.any() and torch.equal(out[a:b][only], alone[only])
+    assert (out[times == 0] == 3).all()
 
 
 def test_a_thread_that_has_called_nothing_yet():
