@@ -4,7 +4,22 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace kivi {
+
+// SMs of the current device, asked once per device.
+inline cudaError_t device_sms(int *sms) {
+  static std::atomic<int> known[64];  // 0: not asked yet
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  *sms = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (*sms) return cudaSuccess;
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
+  return e;
+}
 
 // `bits` is the code width, 2 or 4.
 cudaError_t launch_key_groups(const uint16_t *in, int64_t in_head_stride, int64_t heads, int64_t groups_per_head,
@@ -192,7 +207,7 @@ struct PackedAttentionArgs {
   int Hq, Hkv;
   float softmax_scale;
 };
-bool packed_attention_fits(const PackedAttentionArgs &a);  // the launch's grid
+bool packed_attention_fits(const PackedAttentionArgs &a);  // its blocks are counted in 31 bits
 cudaError_t launch_packed_attention(const PackedAttentionArgs &a, cudaStream_t st);
 
 // The packed prompts quantized into the pages of their sequences.

@@ -778,24 +778,19 @@ int64_t blocks_of(const PackedAttentionArgs &a) {
   return ((int64_t)a.T / (2 * kRows / pack) + a.n_seqs) * (a.Hq / pack);
 }
 
-// The current device and its SMs.  Once per device: the shared memory's limit, and that the kernel has
-// the registers that the warpgroups' split of them rests on.
-cudaError_t prepare_kernel(int *device, int *sms) {
-  static std::atomic<int> known[64];  // SMs + 1 of a device that is ready, else 0
+// The current device.  Once per device: the shared memory's limit, and that the kernel has the
+// registers that the warpgroups' split of them rests on.
+cudaError_t prepare_kernel(int *device) {
+  static std::atomic<bool> ready[64];
   cudaError_t e = cudaGetDevice(device);
   if (e != cudaSuccess) return e;
   const int dev = *device;
-  const int n = dev < 64 ? known[dev].load(std::memory_order_acquire) : 0;
-  if (n) {
-    *sms = n - 1;
-    return cudaSuccess;
-  }
+  if (dev < 64 && ready[dev].load(std::memory_order_acquire)) return cudaSuccess;
   cudaFuncAttributes f;
   if ((e = cudaFuncGetAttributes(&f, packed_attention_kernel)) != cudaSuccess) return e;
   if (f.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
   e = cudaFuncSetAttribute(packed_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess && dev < 64) known[dev].store(*sms + 1, std::memory_order_release);
+  if (e == cudaSuccess && dev < 64) ready[dev].store(true, std::memory_order_release);
   return e;
 }
 
@@ -806,7 +801,8 @@ bool packed_attention_fits(const PackedAttentionArgs &a) { return blocks_of(a) <
 cudaError_t launch_packed_attention(const PackedAttentionArgs &a, cudaStream_t st) {
   const int pack = pack_of(a);
   int dev = 0, sms = 0;
-  cudaError_t e = prepare_kernel(&dev, &sms);
+  cudaError_t e = prepare_kernel(&dev);
+  if (e == cudaSuccess) e = device_sms(&sms);
   if (e != cudaSuccess) return e;
   Maps maps;
   if (!encode_all(&maps, a, pack)) {

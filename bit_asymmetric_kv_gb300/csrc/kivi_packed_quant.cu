@@ -31,7 +31,7 @@ namespace {
 constexpr int kQUnit = 64, kQThreads = 128;
 
 static_assert(kPackedMaxSeqs == kPagedMaxBatch, "a packed batch is a paged batch");
-constexpr int kQCtas = 7, kQGrid = 152 * kQCtas;  // CTAs that fit on an SM (registers), and of a launch
+constexpr int kQCtas = 7;  // CTAs that fit on an SM (registers): a launch is one wave of them
 
 // Where a run of units stands.
 struct UnitWalk {
@@ -354,8 +354,11 @@ __global__ void __launch_bounds__(kQThreads, kQCtas) packed_quantize_kernel(cons
 }  // namespace
 
 cudaError_t launch_packed_quantize(const PackedQuantArgs &a, cudaStream_t st) {
-  const int64_t items = ((int64_t)a.T / kQUnit + a.B) * a.Hkv * 2;
-  const unsigned grid = (unsigned)(items < kQGrid ? items : kQGrid);
+  int sms = 0;
+  const cudaError_t e = device_sms(&sms);
+  if (e != cudaSuccess) return e;
+  const int64_t items = ((int64_t)a.T / kQUnit + a.B) * a.Hkv * 2, wave = (int64_t)sms * kQCtas;
+  const unsigned grid = (unsigned)(items < wave ? items : wave);
   if (a.bits == 2)
     packed_quantize_kernel<2><<<grid, kQThreads, 0, st>>>(a);
   else

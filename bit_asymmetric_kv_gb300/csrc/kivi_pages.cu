@@ -480,7 +480,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
 // Moved pages, and the table's entries.  A warp copies pieces of 4 KB (8 x 16 bytes a lane in
 // flight: with 16 warps an SM, more than the memory's latency needs), so that pages of any
 // size keep every SM busy.
-constexpr int kMoveThreads = 256, kMoveGrid = 152 * 4, kPiece = 4096;
+constexpr int kMoveThreads = 256, kMoveCtas = 4, kPiece = 4096;  // CTAs an SM
 
 __global__ void __launch_bounds__(kMoveThreads) pool_move_kernel(const PoolArgs a, const Ws ws) {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
@@ -567,11 +567,13 @@ cudaError_t launch_pool_reorder(const PoolArgs &a, cudaStream_t st) {
 }
 
 cudaError_t launch_pool_compact(const PoolArgs &a, cudaStream_t st) {
+  int sms = 0;
+  cudaError_t e = device_sms(&sms);
+  if (e != cudaSuccess) return e;
   const Ws ws = workspace_of(a);
   pool_compact_kernel<<<kPoolCtas, kPoolThreads, 0, st>>>(a, ws);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  return launch_behind(pool_move_kernel, dim3(kMoveGrid), kMoveThreads, st, a, ws);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_behind(pool_move_kernel, dim3((unsigned)(sms * kMoveCtas)), kMoveThreads, st, a, ws);
 }
 
 }  // namespace kivi
