@@ -38,9 +38,10 @@
 // as keys they are masked by causality; as values they would meet probability 0, and a NaN
 // there would spread, so the MMA warp overwrites them with zeros first.
 //
-// Measured (two prompts of 16384 and 8200 tokens, 32 query heads on 8): 1.95 ms, 1.41
-// PFLOP/s of causal work, 0.75 of the measured bf16 peak; eight ragged prompts of up to
-// 4113 tokens with 32 KV heads: 0.47 ms, 0.60 of it; 128 prompts of up to 512 tokens: 69 us.
+// Measured with inputs that L2 does not hold (two prompts of 16384 and 8200 tokens, 32 query
+// heads on 8): 2.04 ms, 1.35 PFLOP/s of causal work, 0.72 of the measured bf16 peak; eight ragged
+// prompts of up to 4113 tokens with 32 KV heads: 0.49 ms, 0.57 of it; 128 prompts of up to 512
+// tokens: 70 us.
 // What bounds it: per pass, a tile's softmax (about 1300 cycles, of which the exponential
 // unit needs 512) and its P.V and next scores (1024 of MMAs and about 400 of waits for
 // barriers) come one after the other, and the two tiles overlap only in part.  Tried and
@@ -762,9 +763,11 @@ int pack_of(const PackedAttentionArgs &a) {
 }
 
 // Sets of head groups whose K and V fit in 96 MB of the 129 MB of L2.  Eight ragged prompts of 18
-// thousand tokens together with 32 KV heads (300 MB of K and V), inputs cold: 487 us in four
-// sets, 512 in one; with sets of half the heads and no turning of the order, 506 to 488 us
-// against 469 with inputs that L2 had held.  Where one set holds all, nothing changes.
+// thousand tokens together with 32 KV heads (300 MB of K and V), inputs cold: 487 us and 0.70 GB
+// read from memory in four sets, 514 us and 1.86 GB in one; with sets of half the heads and no
+// turning of the order, 506 to 488 us against 469 with inputs that L2 had held.  Two prompts of 25
+// thousand tokens with 8 KV heads lie just above the bound: 2035 us and 0.33 GB in two sets, 2050 us
+// and 0.55 GB in one.  Where one set holds all, nothing changes.
 unsigned sets_of(const PackedAttentionArgs &a, int pack) {
   const int64_t per_head = (int64_t)a.T * kD * 2 * 2;
   const int64_t heads = std::max<int64_t>(1, (96ll << 20) / per_head);  // KV heads of a set

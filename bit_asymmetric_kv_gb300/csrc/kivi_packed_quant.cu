@@ -14,9 +14,9 @@
 // held by 4 lanes.
 //
 // Measured on 16 prompts of up to 8192 tokens, 8 KV heads, G = 64: 43 us, 0.55 of the measured
-// copy bandwidth.  Bound by instructions: the integer and comparison unit is busy for 53% of
-// the cycles, as is the scheduler, and waits for the first loads and for code that every warp
-// reads anew take the rest.  Units found one by one by a CTA each took 58 us, keys held as
+// copy bandwidth.  No unit is full: the integer and comparison unit is busy for 53% of the
+// cycles, as is the scheduler; waits for a unit's loads, which go out when the unit before is
+// stored, and for code that every warp reads anew take the rest.  Units found one by one by a CTA each took 58 us, keys held as
 // column pairs of 32 rows (packed by a transpose across lanes) too; keys and values of a unit in
 // one pass at five CTAs an SM 45 us; codes put together by logic instead of sums (below) 46 us;
 // five to nine CTAs an SM 44 to 49 us.
