@@ -3,6 +3,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/kivi.h"
 #include "kivi_internal.h"
 
@@ -664,6 +666,50 @@ int kivi_prefill_attention_packed(int32_t Hq, int32_t Hkv, int32_t D, int32_t n_
   if (!kivi::packed_attention_fits(a)) return KIVI_ERR_UNSUPPORTED;
   if (n_tokens == 0) return KIVI_OK;
   return cuda_status(kivi::launch_packed_attention(a, st));
+}
+
+int kivi_prefill_attention_window(int32_t Hq, int32_t Hkv, int32_t D, int32_t n_seqs, const int32_t *cu_seqlens,
+                                  int64_t n_tokens, const int32_t *cu_seqlens_kv, int64_t n_kv_tokens,
+                                  const kivi_rows *q, const kivi_rows *k, const kivi_rows *v, float softmax_scale,
+                                  int32_t window, int32_t sinks, const kivi_rows *out, cudaStream_t st) {
+  if (Hq <= 0 || Hkv <= 0) return KIVI_ERR_ARG;
+  if (D != 128 || Hq % Hkv != 0) return KIVI_ERR_UNSUPPORTED;
+  int s = check_packed(n_seqs, cu_seqlens, n_tokens);
+  if (s != KIVI_OK) return s;
+  if (cu_seqlens_kv) {
+    if ((s = check_packed(n_seqs, cu_seqlens_kv, n_kv_tokens)) != KIVI_OK) return s;
+  } else if (n_kv_tokens != n_tokens) {
+    return KIVI_ERR_ARG;
+  }
+  for (const kivi_rows *r : {q, out})
+    if ((s = check_rows(r)) != KIVI_OK) return s;
+  if (n_kv_tokens > 0)
+    for (const kivi_rows *r : {k, v})
+      if ((s = check_rows(r)) != KIVI_OK) return s;
+  if (!rows_apart(out, n_tokens, Hq)) return KIVI_ERR_ARG;
+  if (!(softmax_scale > 0.f) || !(softmax_scale <= 0x1p127f)) return KIVI_ERR_ARG;
+  if (window <= 0 || sinks < 0) return KIVI_ERR_ARG;
+  kivi::WindowAttentionArgs a = {};
+  a.q = packed_rows(q);
+  a.out = packed_rows(out);
+  if (n_kv_tokens > 0) {
+    a.k = packed_rows(k);
+    a.v = packed_rows(v);
+  }
+  a.cu = cu_seqlens;
+  a.cu_kv = cu_seqlens_kv ? cu_seqlens_kv : cu_seqlens;
+  a.n_seqs = n_seqs;
+  a.T = (int)n_tokens;
+  a.Tk = (int)n_kv_tokens;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  // beyond the keys there is nothing to see: positions stay far from 32 bits
+  a.window = std::min(window, std::max(a.Tk, 1));
+  a.sinks = std::min(sinks, a.Tk);
+  a.softmax_scale = softmax_scale;
+  if (!kivi::window_attention_fits(a)) return KIVI_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return KIVI_OK;
+  return cuda_status(kivi::launch_window_attention(a, st));
 }
 
 int kivi_paged_prefill_packed(const kivi_paged_dims *d, const kivi_paged_cache *c, const int32_t *cu_seqlens,

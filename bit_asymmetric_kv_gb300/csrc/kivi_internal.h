@@ -210,6 +210,19 @@ struct PackedAttentionArgs {
 bool packed_attention_fits(const PackedAttentionArgs &a);  // its blocks are counted in 31 bits
 cudaError_t launch_packed_attention(const PackedAttentionArgs &a, cudaStream_t st);
 
+// The same with a sliding window and sinks, the queries being the last rows of their sequence's keys.
+struct WindowAttentionArgs {
+  PackedRows q, k, v, out;
+  const int32_t *cu, *cu_kv;  // [n_seqs + 1] row bounds of the queries, of the keys
+  int n_seqs;                 // <= kPackedMaxSeqs
+  int T, Tk;                  // rows of the two axes
+  int Hq, Hkv;
+  int window, sinks;          // 1 .. max(Tk, 1), 0 .. Tk
+  float softmax_scale;
+};
+bool window_attention_fits(const WindowAttentionArgs &a);
+cudaError_t launch_window_attention(const WindowAttentionArgs &a, cudaStream_t st);
+
 // The packed prompts quantized into the pages of their sequences.
 struct PackedQuantArgs {
   PackedRows k, v;

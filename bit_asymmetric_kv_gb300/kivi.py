@@ -105,12 +105,14 @@ def lib() -> ctypes.CDLL:
             getattr(L, name).restype = ctypes.c_int
         PR, PP = ctypes.POINTER(kivi_rows), ctypes.POINTER(kivi_page_pool)
         L.kivi_prefill_attention_packed.argtypes = [i32, i32, i32, i32, P, i64, PR, PR, PR, ctypes.c_float, PR, P]
+        L.kivi_prefill_attention_window.argtypes = [i32, i32, i32, i32, P, i64, P, i64, PR, PR, PR, ctypes.c_float, i32,
+                                                    i32, PR, P]
         L.kivi_paged_prefill_packed.argtypes = [PD, PC, P, i64, PR, PR, P]
         L.kivi_paged_pool_workspace_bytes.argtypes = [PD]
         L.kivi_paged_pool_workspace_bytes.restype = sz
         for name in ("kivi_paged_reserve", "kivi_paged_reorder", "kivi_paged_compact"):
             getattr(L, name).argtypes = [PD, PC, PP, P, P, sz, P]
-        for name in ("kivi_prefill_attention_packed", "kivi_paged_prefill_packed", "kivi_paged_reserve",
+        for name in ("kivi_prefill_attention_packed", "kivi_prefill_attention_window", "kivi_paged_prefill_packed", "kivi_paged_reserve",
                      "kivi_paged_reorder", "kivi_paged_compact"):
             getattr(L, name).restype = ctypes.c_int
         L.kivi_status_string.argtypes = [ctypes.c_int]
@@ -519,6 +521,46 @@ def kivi_prefill_attention_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Ten
     if T:
         _run("kivi_prefill_attention_packed", dev, stream, Hq, kv[1], D, bounds - 1, cu, T, rq, rk, rv,
              float(softmax_scale), ro)
+    return out
+
+
+def _count(x: int, name: str, least: int) -> int:
+    """A number of positions as the ABI's int32: at least `least`; one beyond int32 sees what the largest does."""
+    if x < least:
+        raise ValueError(f"{name}: expected at least {least}")
+    return min(int(x), 2**31 - 1)
+
+
+def kivi_prefill_attention_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                                  window: int, sinks: int, softmax_scale: float,
+                                  cu_seqlens_kv: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                                  stream=None) -> torch.Tensor:
+    """kivi_prefill_attention_packed in which position p sees the positions p - window + 1 .. p and the
+    first `sinks`.  With cu_seqlens_kv (int32 [n_seqs + 1]) k and v have a token axis of their own,
+    [Tk, Hkv, D], and the queries of a sequence are its last tokens; a query before the first key
+    gets zeros."""
+    dev = q.device
+    rq = _rows(q, "q", dev)
+    shape, kv = q.shape, k.shape
+    T, Hq, D = shape
+    if kv != v.shape or len(kv) != 3 or kv[2] != D or (cu_seqlens_kv is None and kv[0] != T):
+        raise ValueError(f"q {list(shape)}, k {list(kv)}, v {list(v.shape)} do not fit together")
+    rk, rv = _rows(k, "k", dev), _rows(v, "v", dev)
+    bounds = cu_seqlens.numel()
+    if bounds < 2:
+        raise ValueError("cu_seqlens holds at least two bounds")
+    cu = _i32(cu_seqlens, "cu_seqlens", bounds, dev)
+    cu_kv = None if cu_seqlens_kv is None else _i32(cu_seqlens_kv, "cu_seqlens_kv", bounds, dev)
+    window, sinks = _count(window, "window", 1), _count(sinks, "sinks", 0)
+    if out is None:
+        with _allocating_on(dev, stream):
+            out = torch.zeros(shape, dtype=torch.float16, device=dev)
+    elif out.shape != shape:
+        raise ValueError(f"out: expected shape {list(shape)}")
+    ro = _rows(out, "out", dev)
+    if T:
+        _run("kivi_prefill_attention_window", dev, stream, Hq, kv[1], D, bounds - 1, cu, T, cu_kv, kv[0], rq, rk, rv,
+             float(softmax_scale), window, sinks, ro)
     return out
 
 

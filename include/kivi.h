@@ -427,6 +427,29 @@ KIVI_API int kivi_prefill_attention_packed(int32_t Hq, int32_t Hkv, int32_t D, i
                                            const kivi_rows *out, cudaStream_t stream);
 
 /*
+ * kivi_prefill_attention_packed with a sliding window and sinks, for prompts and for chunks behind
+ * earlier tokens.  Queries and keys have token axes of their own: sequence s has the rows
+ * cu_seqlens[s] .. cu_seqlens[s + 1] - 1 of q and out (n_tokens rows) and the rows cu_seqlens_kv[s] ..
+ * cu_seqlens_kv[s + 1] - 1 of k and v (n_kv_tokens rows), and its queries are its last tokens: with n
+ * queries and m keys, query i stands at position p = i + m - n.  cu_seqlens_kv == NULL: the
+ * same rows (n_kv_tokens == n_tokens, else KIVI_ERR_ARG).  Position p sees position j when
+ *   p - window < j <= p   or   j < sinks and j <= p;
+ * window >= 1 counts p itself, sinks >= 0 (KIVI_ERR_ARG), either as large as one likes.
+ * Positions count the rows given: where the keys are the first `sinks` tokens of a longer sequence and
+ * its newest ones side by side (kivi_paged_read), and the newest reach back to the first query's window,
+ * the result is that of the whole sequence.
+ * A query that sees nothing (p < 0: fewer keys than queries) gets zeros.  Keys and values that no query of
+ * the call sees are not used, whatever they hold; what is seen must be finite.  Everything else is as for
+ * kivi_prefill_attention_packed; with n_kv_tokens == 0, k and v are not looked at.
+ */
+KIVI_API int kivi_prefill_attention_window(int32_t Hq, int32_t Hkv, int32_t D, int32_t n_seqs,
+                                           const int32_t *cu_seqlens, int64_t n_tokens,
+                                           const int32_t *cu_seqlens_kv, int64_t n_kv_tokens, const kivi_rows *q,
+                                           const kivi_rows *k, const kivi_rows *v, float softmax_scale,
+                                           int32_t window, int32_t sinks, const kivi_rows *out,
+                                           cudaStream_t stream);
+
+/*
  * Quantize the packed prompts of a paged batch into their pages, sequence s of the pack
  * into sequence s of the cache (n_seqs = dims->B), each as kivi_paged_prefill does for
  * one: codes, scales, zeros and residual bit for bit, and seq_lens[s] = its length.  An

@@ -1,0 +1,65 @@
+"""Sliding-window calls: what the C ABI and the Python binding refuse, on the host and before any
+launch.  No test here touches device memory."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+from bit_asymmetric_kv_gb300 import build as kbuild
+from bit_asymmetric_kv_gb300 import kivi
+
+FAKE = 1 << 20  # an aligned, never dereferenced address
+
+
+@pytest.fixture(scope="module")
+def L():
+    kbuild.build()
+    return kivi.lib()
+
+
+def _rows(data=FAKE, ts=1024, hs=128):
+    return kivi.kivi_rows(data, ts, hs)
+
+
+def _attention(L, Hq=8, Hkv=2, D=128, n_seqs=3, cu=FAKE, T=100, cu_kv=FAKE, Tk=200, q=None, k=None, v=None, scale=0.1,
+               window=10, sinks=4, out=None):
+    rows = [r or _rows() for r in (q, k, v, out)]
+    return L.kivi_prefill_attention_window(Hq, Hkv, D, n_seqs, cu, T, cu_kv, Tk, rows[0], rows[1], rows[2], scale,
+                                           window, sinks, rows[3], 0)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(Hq=0), 1), (dict(Hkv=0), 1), (dict(Hq=7), 3), (dict(D=64), 3), (dict(n_seqs=0), 1), (dict(n_seqs=513), 3),
+    (dict(cu=0), 1), (dict(cu=FAKE + 2), 2), (dict(T=-1), 1), (dict(T=1 << 31), 3),
+    (dict(cu_kv=0), 1),                          # the same rows, and another number of them
+    (dict(cu_kv=FAKE + 1), 2), (dict(Tk=-1), 1), (dict(Tk=1 << 31), 3),
+    (dict(window=0), 1), (dict(window=-5), 1), (dict(sinks=-1), 1),
+    (dict(q=_rows(0)), 1), (dict(k=_rows(0)), 1), (dict(v=_rows(0)), 1), (dict(out=_rows(0)), 1),
+    (dict(q=_rows(FAKE + 8)), 2), (dict(v=_rows(ts=1028)), 2), (dict(k=_rows(hs=132)), 2), (dict(k=_rows(hs=0)), 1),
+    (dict(v=_rows(ts=(1 << 38) + 8)), 3), (dict(scale=0.0), 1), (dict(scale=math.inf), 1), (dict(scale=math.nan), 1),
+    (dict(out=_rows(ts=128, hs=128)), 1),        # every head of a token on the next token's first
+    (dict(T=2**31 - 1, Hq=4096, Hkv=4096, out=_rows(ts=4096 * 128)), 3),  # more blocks than a grid holds
+])
+def test_attention_refuses(L, bad, status):
+    assert _attention(L, **bad) == status
+
+
+def test_attention_of_nothing_launches_nothing(L):
+    assert _attention(L, T=0) == 0
+    assert _attention(L, T=0, Tk=0, k=_rows(0), v=_rows(0)) == 0
+    assert _attention(L, T=0, Tk=0, cu_kv=0) == 0
+
+
+def test_binding_refuses(L):
+    half = torch.zeros((4, 2, 128), dtype=torch.float16)
+    cu = torch.tensor([0, 4], dtype=torch.int32)
+    with pytest.raises(TypeError):  # host tensors
+        kivi.kivi_prefill_attention_window(half, half, half, cu, 4, 0, 0.1)
+    assert kivi._count(2**40, "window", 1) == 2**31 - 1
+    for bad in (0, -3):
+        with pytest.raises(ValueError):
+            kivi._count(bad, "window", 1)
+    with pytest.raises(ValueError):
+        kivi._count(-1, "sinks", 0)
