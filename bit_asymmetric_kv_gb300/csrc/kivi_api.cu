@@ -599,45 +599,61 @@ size_t kivi_paged_decode_workspace_bytes(const kivi_paged_dims *d, int32_t Hq) {
   return g.ws_bytes;
 }
 
-int kivi_paged_decode_attention(const kivi_paged_dims *d, const kivi_paged_cache *c, const uint16_t *q, int32_t Hq,
-                                float softmax_scale, uint16_t *out, void *ws, size_t ws_bytes, cudaStream_t st) {
+// The four paged decode calls: k_new and v_new null for the attention alone, window 0 for the whole context.
+static int paged_decode(const kivi_paged_dims *d, const kivi_paged_cache *c, bool step, const uint16_t *k_new,
+                        const uint16_t *v_new, const uint16_t *q, int32_t Hq, float softmax_scale, int32_t window,
+                        int32_t sinks, uint16_t *out, void *ws, size_t ws_bytes, cudaStream_t st) {
   int s = check_paged_dims(d);
   if (s != KIVI_OK) return s;
   if ((s = check_paged_cache(d, c)) != KIVI_OK) return s;
   if ((s = check_paged_heads(d, Hq)) != KIVI_OK) return s;
-  if (!q || !out) return KIVI_ERR_ARG;
-  if (!aligned16(q) || !aligned16(out)) return KIVI_ERR_ALIGN;
+  if ((step && (!k_new || !v_new)) || !q || !out) return KIVI_ERR_ARG;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(q) || !aligned16(out)) return KIVI_ERR_ALIGN;
   kivi::PagedGeom g;
-  if (kivi::paged_decode_geometry(d->B, d->Hkv, Hq, d->G, d->bits, &g) != cudaSuccess) return KIVI_ERR_CUDA;
+  if (kivi::paged_decode_geometry(d->B, d->Hkv, Hq, d->G, d->bits, &g, window > 0) != cudaSuccess) return KIVI_ERR_CUDA;
   if (!ws || ws_bytes < g.ws_bytes) return KIVI_ERR_WORKSPACE;
   if (!aligned16(ws)) return KIVI_ERR_ALIGN;
-  const kivi::DecodeArgs a = paged_decode_args(d, c, q, Hq, softmax_scale, out, ws, g);
+  kivi::DecodeArgs a = paged_decode_args(d, c, q, Hq, softmax_scale, out, ws, g);
+  // beyond the capacity there is nothing to see
+  a.window = std::min<int64_t>(window, paged_cap(d));
+  a.sinks = std::min<int64_t>(sinks, paged_cap(d));
+  if (step) {
+    // 1. append (flushing the groups that fill), lengths unchanged
+    const cudaError_t e = kivi::launch_paged_append(paged_append_args(d, c, k_new, v_new), st);
+    if ((s = cuda_status(e)) != KIVI_OK) return s;
+    // 2. attention over seq_lens + 1 tokens, overlapping the append; its combine
+    //    advances the lengths once everything before it has completed
+    a.wait_tail = 1;
+    a.len_offset = 1;
+    a.advance_lens = c->seq_lens;
+  }
   return cuda_status(kivi::launch_paged_decode(a, st));
+}
+
+int kivi_paged_decode_attention(const kivi_paged_dims *d, const kivi_paged_cache *c, const uint16_t *q, int32_t Hq,
+                                float softmax_scale, uint16_t *out, void *ws, size_t ws_bytes, cudaStream_t st) {
+  return paged_decode(d, c, false, nullptr, nullptr, q, Hq, softmax_scale, 0, 0, out, ws, ws_bytes, st);
 }
 
 int kivi_paged_decode_step(const kivi_paged_dims *d, const kivi_paged_cache *c, const uint16_t *k_new,
                            const uint16_t *v_new, const uint16_t *q, int32_t Hq, float softmax_scale, uint16_t *out,
                            void *ws, size_t ws_bytes, cudaStream_t st) {
-  int s = check_paged_dims(d);
-  if (s != KIVI_OK) return s;
-  if ((s = check_paged_cache(d, c)) != KIVI_OK) return s;
-  if ((s = check_paged_heads(d, Hq)) != KIVI_OK) return s;
-  if (!k_new || !v_new || !q || !out) return KIVI_ERR_ARG;
-  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(q) || !aligned16(out)) return KIVI_ERR_ALIGN;
-  kivi::PagedGeom g;
-  if (kivi::paged_decode_geometry(d->B, d->Hkv, Hq, d->G, d->bits, &g) != cudaSuccess) return KIVI_ERR_CUDA;
-  if (!ws || ws_bytes < g.ws_bytes) return KIVI_ERR_WORKSPACE;
-  if (!aligned16(ws)) return KIVI_ERR_ALIGN;
-  // 1. append (flushing the groups that fill), lengths unchanged
-  cudaError_t e = kivi::launch_paged_append(paged_append_args(d, c, k_new, v_new), st);
-  if ((s = cuda_status(e)) != KIVI_OK) return s;
-  // 2. attention over seq_lens + 1 tokens, overlapping the append; its combine
-  //    advances the lengths once everything before it has completed
-  kivi::DecodeArgs a = paged_decode_args(d, c, q, Hq, softmax_scale, out, ws, g);
-  a.wait_tail = 1;
-  a.len_offset = 1;
-  a.advance_lens = c->seq_lens;
-  return cuda_status(kivi::launch_paged_decode(a, st));
+  return paged_decode(d, c, true, k_new, v_new, q, Hq, softmax_scale, 0, 0, out, ws, ws_bytes, st);
+}
+
+int kivi_paged_decode_attention_window(const kivi_paged_dims *d, const kivi_paged_cache *c, const uint16_t *q,
+                                       int32_t Hq, float softmax_scale, int32_t window, int32_t sinks, uint16_t *out,
+                                       void *ws, size_t ws_bytes, cudaStream_t st) {
+  if (window <= 0 || sinks < 0) return KIVI_ERR_ARG;
+  return paged_decode(d, c, false, nullptr, nullptr, q, Hq, softmax_scale, window, sinks, out, ws, ws_bytes, st);
+}
+
+int kivi_paged_decode_step_window(const kivi_paged_dims *d, const kivi_paged_cache *c, const uint16_t *k_new,
+                                  const uint16_t *v_new, const uint16_t *q, int32_t Hq, float softmax_scale,
+                                  int32_t window, int32_t sinks, uint16_t *out, void *ws, size_t ws_bytes,
+                                  cudaStream_t st) {
+  if (window <= 0 || sinks < 0) return KIVI_ERR_ARG;
+  return paged_decode(d, c, true, k_new, v_new, q, Hq, softmax_scale, window, sinks, out, ws, ws_bytes, st);
 }
 
 // --------------------------------------------------------------------- packed prompts

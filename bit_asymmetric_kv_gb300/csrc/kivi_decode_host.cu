@@ -1,5 +1,5 @@
 // kivi_decode_host.cu -- grid sizing and launches of the decode kernels in
-// kivi_decode.cu (host code only, so that the kernels' source is one file).
+// kivi_decode_body.cuh (host code only).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -150,11 +150,16 @@ cudaError_t decode_geometry(int B, int Hkv, int Hq, int G, int bits, int64_t n, 
   return cudaSuccess;
 }
 
-cudaError_t paged_decode_geometry(int B, int Hkv, int Hq, int G, int bits, PagedGeom *out) {
+cudaError_t paged_decode_geometry(int B, int Hkv, int Hq, int G, int bits, PagedGeom *out, bool window) {
   const int R = Hq / Hkv;
   int nw = 0;
   cudaError_t e = warps_on_device(decode_kernels(R, G, bits, true, B), &nw);
   if (e != cudaSuccess) return e;
+  // the window's kernel is asked about here too, so that any call or query before a graph's
+  // capture has both kernels' answers on record
+  int win = 0;
+  if ((e = warps_on_device(decode_window_kernels(R, G, bits, B), &win)) != cudaSuccess) return e;
+  if (window && win < nw) nw = win;
   const size_t heads = (size_t)B * Hkv;
   out->n_warps = nw;
   out->grid = nw / kDecodeWarps;
@@ -193,7 +198,8 @@ cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t st) {
 }
 
 cudaError_t launch_paged_decode(const DecodeArgs &a, cudaStream_t st) {
-  const DecodeKernels k = decode_kernels(a.Hq / a.Hkv, a.G, a.bits, true, a.B);
+  const int R = a.Hq / a.Hkv;
+  const DecodeKernels k = a.window ? decode_window_kernels(R, a.G, a.bits, a.B) : decode_kernels(R, a.G, a.bits, true, a.B);
   const float *ws = a.ws;
   int Hkv = a.Hkv, Hq = a.Hq, B = a.B;
   int32_t *advance = a.advance_lens;

@@ -105,9 +105,12 @@ struct DecodeArgs {
   int max_pages;
   int len_offset;              // tokens appended just before (0 or 1): the context is seq_lens[b] + len_offset
   int32_t cap_tokens;          // max_pages << page_shift
+  // paged layout with a window: the last token sees the newest `window` tokens and the first `sinks`
+  int window;                  // 0: the whole context
+  int sinks;
 };
 
-// Decode kernels (kivi_decode.cu) and their launch shape.  The host side
+// Decode kernels (kivi_decode.cu, kivi_decode_body.cuh) and their launch shape.  The host side
 // (kivi_decode_host.cu) sizes the grid from the occupancy of `decode` with `smem`
 // bytes of dynamic shared memory; `smem_limit` is the most any launch of it uses.
 constexpr int kDecodeWarps = 4;   // warps per decode CTA
@@ -134,6 +137,8 @@ struct DecodeKernels {
 // vg: channels per value scale (128, or 64 / 32 for value channel groups: dense
 // 2-bit caches only, no small-context kernel).
 DecodeKernels decode_kernels(int R, int G, int bits, bool paged, int B, int vg = 128);
+// Those of the paged layout with a window (kivi_decode_window.cu).
+DecodeKernels decode_window_kernels(int R, int G, int bits, int B);
 
 // Geometry of one decode call on the current device (deterministic for given sizes).
 struct DecodeGeom {
@@ -157,7 +162,9 @@ struct PagedGeom {
   size_t ws_bytes;
 };
 constexpr int kPagedMaxBatch = 512;
-cudaError_t paged_decode_geometry(int B, int Hkv, int Hq, int G, int bits, PagedGeom *out);
+// `window`: of the kernel over a window.  It never has more warps than the other: one workspace
+// serves both.
+cudaError_t paged_decode_geometry(int B, int Hkv, int Hq, int G, int bits, PagedGeom *out, bool window = false);
 cudaError_t launch_paged_decode(const DecodeArgs &a, cudaStream_t st);
 
 // Fused prefill (kivi_prefill.cu): causal attention over the fp16 prompt and, when

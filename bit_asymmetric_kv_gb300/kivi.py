@@ -100,8 +100,11 @@ def lib() -> ctypes.CDLL:
         L.kivi_paged_decode_workspace_bytes.restype = sz
         L.kivi_paged_decode_attention.argtypes = [PD, PC, P, i32, ctypes.c_float, P, P, sz, P]
         L.kivi_paged_decode_step.argtypes = [PD, PC, P, P, P, i32, ctypes.c_float, P, P, sz, P]
+        L.kivi_paged_decode_attention_window.argtypes = [PD, PC, P, i32, ctypes.c_float, i32, i32, P, P, sz, P]
+        L.kivi_paged_decode_step_window.argtypes = [PD, PC, P, P, P, i32, ctypes.c_float, i32, i32, P, P, sz, P]
         for name in ("kivi_paged_buffer_bytes", "kivi_paged_prefill", "kivi_paged_append_token",
-                     "kivi_paged_decode_attention", "kivi_paged_decode_step"):
+                     "kivi_paged_decode_attention", "kivi_paged_decode_step", "kivi_paged_decode_attention_window",
+                     "kivi_paged_decode_step_window"):
             getattr(L, name).restype = ctypes.c_int
         PR, PP = ctypes.POINTER(kivi_rows), ctypes.POINTER(kivi_page_pool)
         L.kivi_prefill_attention_packed.argtypes = [i32, i32, i32, i32, P, i64, PR, PR, PR, ctypes.c_float, PR, P]
@@ -562,6 +565,51 @@ def kivi_prefill_attention_window(q: torch.Tensor, k: torch.Tensor, v: torch.Ten
         _run("kivi_prefill_attention_window", dev, stream, Hq, kv[1], D, bounds - 1, cu, T, cu_kv, kv[0], rq, rk, rv,
              float(softmax_scale), window, sinks, ro)
     return out
+
+
+def _heads(t: torch.Tensor, name: str, cache: PagedCache, heads: int | None = None) -> torch.Tensor:
+    """An fp16 tensor [B, heads, D] of one token a sequence, contiguous and on the cache's device."""
+    d = cache.dims
+    _f16(t, name)
+    if t.device != cache.k_codes.device:
+        raise ValueError(f"{name}: expected a tensor on {cache.k_codes.device}")
+    if t.dim() != 3 or t.shape[0] != d.B or t.shape[2] != d.D or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name}: {list(t.shape)}, expected [{d.B}, {heads or 'heads'}, {d.D}]")
+    return t
+
+
+def _decode_window(call: str, cache: PagedCache, new: list, q: torch.Tensor, window: int, sinks: int,
+                   softmax_scale: float, out: torch.Tensor | None, ws: torch.Tensor | None, stream) -> torch.Tensor:
+    dev, Hq = cache.k_codes.device, _heads(q, "q", cache).shape[1]
+    window, sinks = _count(window, "window", 1), _count(sinks, "sinks", 0)
+    if out is None or ws is None:
+        with _allocating_on(dev, stream):
+            out = torch.empty_like(q) if out is None else out
+            ws = paged_workspace(cache, Hq, device=dev) if ws is None else ws
+    _heads(out, "out", cache, Hq)
+    if not ws.is_cuda or ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous tensor on {dev}")
+    _run(call, dev, stream, cache.dims, cache.c, *[t.data_ptr() for t in new], q.data_ptr(), Hq, float(softmax_scale),
+         window, sinks, out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+    return out
+
+
+def kivi_paged_decode_attention_window(cache: PagedCache, q: torch.Tensor, window: int, sinks: int,
+                                       softmax_scale: float, out: torch.Tensor | None = None,
+                                       ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """kivi_paged_decode_attention in which a sequence's newest token sees its newest `window` tokens and its
+    first `sinks`; pages that hold none of these are not read."""
+    return _decode_window("kivi_paged_decode_attention_window", cache, [], q, window, sinks, softmax_scale, out, ws,
+                          stream)
+
+
+def kivi_paged_decode_step_window(cache: PagedCache, k_new: torch.Tensor, v_new: torch.Tensor, q: torch.Tensor,
+                                  window: int, sinks: int, softmax_scale: float, out: torch.Tensor | None = None,
+                                  ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """kivi_paged_decode_step in which the appended token sees the newest `window` tokens, itself among them,
+    and the first `sinks`."""
+    new = [_heads(k_new, "k_new", cache, cache.dims.Hkv), _heads(v_new, "v_new", cache, cache.dims.Hkv)]
+    return _decode_window("kivi_paged_decode_step_window", cache, new, q, window, sinks, softmax_scale, out, ws, stream)
 
 
 def kivi_paged_prefill_packed(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,

@@ -381,6 +381,23 @@ KIVI_API int kivi_paged_decode_step(const kivi_paged_dims *dims, const kivi_page
                                     cudaStream_t stream);
 
 /*
+ * The same two calls with a sliding window and sinks: the newest token, at position p = n - 1 of n, sees
+ * position j when p - window < j or j < sinks.  window >= 1, sinks >= 0 (KIVI_ERR_ARG), either as large as
+ * one likes.  Only the pages that hold a visible token are looked up and read: a page that lies outside the window
+ * and behind the sinks may be given to another sequence, and its table entry hold anything
+ * (kivi_paged_reserve_window does that on the device).  A key group counts as read when a token of it is
+ * visible.  Workspace: kivi_paged_decode_workspace_bytes().
+ */
+KIVI_API int kivi_paged_decode_attention_window(const kivi_paged_dims *dims, const kivi_paged_cache *cache,
+                                                const uint16_t *q, int32_t Hq, float softmax_scale, int32_t window,
+                                                int32_t sinks, uint16_t *out, void *ws, size_t ws_bytes,
+                                                cudaStream_t stream);
+KIVI_API int kivi_paged_decode_step_window(const kivi_paged_dims *dims, const kivi_paged_cache *cache,
+                                           const uint16_t *k_new, const uint16_t *v_new, const uint16_t *q,
+                                           int32_t Hq, float softmax_scale, int32_t window, int32_t sinks,
+                                           uint16_t *out, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
  * ---- Packed prompts ------------------------------------------------------------------
  * Prompts of different lengths side by side in one token axis, as a serving engine
  * admits them: sequence s is rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 of an axis of

@@ -52,6 +52,40 @@ def test_attention_of_nothing_launches_nothing(L):
     assert _attention(L, T=0, Tk=0, cu_kv=0) == 0
 
 
+def _dims(**kw):
+    d = dict(B=2, Hkv=4, D=128, G=32, bits=2, value_residual=0, page_tokens=64, max_pages_per_seq=8, num_pages=20)
+    d.update(kw)
+    return kivi.kivi_paged_dims(*d.values())
+
+
+def _cache(table=FAKE, v_res=0):
+    return kivi.kivi_paged_cache(FAKE, FAKE, FAKE, FAKE, FAKE, v_res, table, FAKE)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(window=0), 1), (dict(window=-1), 1), (dict(sinks=-1), 1), (dict(dims=_dims(B=0)), 1),
+    (dict(dims=_dims(B=513)), 3), (dict(dims=_dims(page_tokens=48)), 3), (dict(dims=_dims(value_residual=1)), 1),
+    (dict(cache=_cache(table=0)), 1), (dict(Hq=0), 1), (dict(Hq=12), 3), (dict(q=0), 1), (dict(out=0), 1),
+    (dict(q=FAKE + 8), 2), (dict(out=FAKE + 2), 2),
+])
+@pytest.mark.parametrize("step", [False, True])
+def test_decode_refuses(L, bad, status, step):
+    a = dict(dims=_dims(), cache=_cache(), q=FAKE, Hq=8, window=5, sinks=1, out=FAKE)
+    a.update(bad)
+    rest = (a["q"], a["Hq"], 0.1, a["window"], a["sinks"], a["out"], FAKE, 1 << 40, 0)
+    if step:
+        assert L.kivi_paged_decode_step_window(a["dims"], a["cache"], FAKE, FAKE, *rest) == status
+    else:
+        assert L.kivi_paged_decode_attention_window(a["dims"], a["cache"], *rest) == status
+
+
+def test_step_refuses_its_token(L):
+    rest = (FAKE, 8, 0.1, 5, 1, FAKE, FAKE, 1 << 40, 0)
+    call = L.kivi_paged_decode_step_window
+    assert call(_dims(), _cache(), 0, FAKE, *rest) == 1 and call(_dims(), _cache(), FAKE, 0, *rest) == 1
+    assert call(_dims(), _cache(), FAKE + 4, FAKE, *rest) == 2 and call(_dims(), _cache(), FAKE, FAKE + 8, *rest) == 2
+
+
 def test_binding_refuses(L):
     half = torch.zeros((4, 2, 128), dtype=torch.float16)
     cu = torch.tensor([0, 4], dtype=torch.int32)
