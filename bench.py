@@ -131,7 +131,7 @@ def kernel_source_sha() -> str:
 
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "bit_asymmetric_kv_gb300", "csrc")
-    for name in ("kivi_decode.cu", "kivi_decode_body.cuh", "kivi_device.cuh", "kivi_internal.h"):  # the decode kernels' sources
+    for name in ("kivi_decode.cu", "kivi_device.cuh", "kivi_internal.h"):  # the decode kernels' sources
         with open(os.path.join(csrc, name), "rb") as f:
             h.update(name.encode() + b"\0" + f.read())
     return h.hexdigest()[:16]

@@ -728,8 +728,9 @@ int kivi_prefill_attention_window(int32_t Hq, int32_t Hkv, int32_t D, int32_t n_
   return cuda_status(kivi::launch_window_attention(a, st));
 }
 
-int kivi_paged_prefill_packed(const kivi_paged_dims *d, const kivi_paged_cache *c, const int32_t *cu_seqlens,
-                              int64_t n_tokens, const kivi_rows *k, const kivi_rows *v, cudaStream_t st) {
+// The packed tokens of a paged batch, written from the start or (extend) behind what is there.
+static int paged_quantize(const kivi_paged_dims *d, const kivi_paged_cache *c, const int32_t *cu_seqlens,
+                          int64_t n_tokens, const kivi_rows *k, const kivi_rows *v, bool extend, cudaStream_t st) {
   int s = check_paged_dims(d);
   if (s != KIVI_OK) return s;
   if ((s = check_paged_cache(d, c)) != KIVI_OK) return s;
@@ -757,7 +758,56 @@ int kivi_paged_prefill_packed(const kivi_paged_dims *d, const kivi_paged_cache *
   a.shift = page_shift_of(d->page_tokens);
   a.max_pages = d->max_pages_per_seq;
   a.T = (int)n_tokens;
-  return cuda_status(kivi::launch_packed_quantize(a, st));
+  return cuda_status(extend ? kivi::launch_packed_extend(a, st) : kivi::launch_packed_quantize(a, st));
+}
+
+int kivi_paged_prefill_packed(const kivi_paged_dims *d, const kivi_paged_cache *c, const int32_t *cu_seqlens,
+                              int64_t n_tokens, const kivi_rows *k, const kivi_rows *v, cudaStream_t st) {
+  return paged_quantize(d, c, cu_seqlens, n_tokens, k, v, false, st);
+}
+
+int kivi_paged_extend_packed(const kivi_paged_dims *d, const kivi_paged_cache *c, const int32_t *cu_seqlens,
+                             int64_t n_tokens, const kivi_rows *k, const kivi_rows *v, cudaStream_t st) {
+  return paged_quantize(d, c, cu_seqlens, n_tokens, k, v, true, st);
+}
+
+int kivi_paged_read(const kivi_paged_dims *d, const kivi_paged_cache *c, const int32_t *cu_seqlens, int64_t n_tokens,
+                    const int32_t *take, int32_t first, const kivi_rows *k_out, const kivi_rows *v_out,
+                    cudaStream_t st) {
+  int s = check_paged_dims(d);
+  if (s != KIVI_OK) return s;
+  if ((s = check_paged_cache(d, c)) != KIVI_OK) return s;
+  if ((s = check_packed(d->B, cu_seqlens, n_tokens)) != KIVI_OK) return s;
+  if (first < 0) return KIVI_ERR_ARG;
+  if (!aligned4(take)) return KIVI_ERR_ALIGN;
+  for (const kivi_rows *r : {k_out, v_out}) {
+    if ((s = check_rows(r)) != KIVI_OK) return s;
+    if (!rows_apart(r, n_tokens, d->Hkv)) return KIVI_ERR_ARG;
+  }
+  if (n_tokens == 0) return KIVI_OK;
+  kivi::ReadArgs a = {};
+  a.k = packed_rows(k_out);
+  a.v = packed_rows(v_out);
+  a.cu = cu_seqlens;
+  a.take = take;
+  a.bt = c->block_table;
+  a.seq_lens = c->seq_lens;
+  a.k_res = c->k_res;
+  a.v_res = paged_vres(d, c);
+  a.k_codes = c->k_codes;
+  a.k_meta = c->k_meta;
+  a.v_codes = c->v_codes;
+  a.v_meta = c->v_meta;
+  a.num_pages = d->num_pages;
+  a.B = d->B;
+  a.Hkv = d->Hkv;
+  a.G = d->G;
+  a.bits = d->bits;
+  a.shift = page_shift_of(d->page_tokens);
+  a.max_pages = d->max_pages_per_seq;
+  a.T = (int)n_tokens;
+  a.first = first;
+  return cuda_status(kivi::launch_paged_read(a, st));
 }
 
 // ------------------------------------------------------------------------------ pages
@@ -772,6 +822,19 @@ int kivi_paged_reserve(const kivi_paged_dims *d, const kivi_paged_cache *c, cons
   if (s != KIVI_OK) return s;
   kivi::PoolArgs a = pool_args(d, c, p, ws);
   a.arg = extra;
+  return cuda_status(kivi::launch_pool_reserve(a, st));
+}
+
+int kivi_paged_reserve_window(const kivi_paged_dims *d, const kivi_paged_cache *c, const kivi_page_pool *p,
+                              const int32_t *extra, int32_t window, int32_t sinks, void *ws, size_t ws_bytes,
+                              cudaStream_t st) {
+  if (window <= 0 || sinks < 0) return KIVI_ERR_ARG;
+  const int s = check_pool(d, c, p, extra, ws, ws_bytes);
+  if (s != KIVI_OK) return s;
+  kivi::PoolArgs a = pool_args(d, c, p, ws);
+  a.arg = extra;
+  a.window = window;
+  a.sinks = sinks;
   return cuda_status(kivi::launch_pool_reserve(a, st));
 }
 

@@ -1,5 +1,5 @@
 // kivi_decode_host.cu -- grid sizing and launches of the decode kernels in
-// kivi_decode_body.cuh (host code only).
+// kivi_decode.cu (host code only, so that the kernels' source is one file).
 #include <cuda_runtime.h>
 #include <stdint.h>
 

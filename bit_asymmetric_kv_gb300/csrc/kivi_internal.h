@@ -110,7 +110,7 @@ struct DecodeArgs {
   int sinks;
 };
 
-// Decode kernels (kivi_decode.cu, kivi_decode_body.cuh) and their launch shape.  The host side
+// Decode kernels (kivi_decode.cu) and their launch shape.  The host side
 // (kivi_decode_host.cu) sizes the grid from the occupancy of `decode` with `smem`
 // bytes of dynamic shared memory; `smem_limit` is the most any launch of it uses.
 constexpr int kDecodeWarps = 4;   // warps per decode CTA
@@ -137,7 +137,7 @@ struct DecodeKernels {
 // vg: channels per value scale (128, or 64 / 32 for value channel groups: dense
 // 2-bit caches only, no small-context kernel).
 DecodeKernels decode_kernels(int R, int G, int bits, bool paged, int B, int vg = 128);
-// Those of the paged layout with a window (kivi_decode_window.cu).
+// Those of the paged layout with a window.
 DecodeKernels decode_window_kernels(int R, int G, int bits, int B);
 
 // Geometry of one decode call on the current device (deterministic for given sizes).
@@ -243,6 +243,23 @@ struct PackedQuantArgs {
   int B, Hkv, G, bits, shift, max_pages, T;
 };
 cudaError_t launch_packed_quantize(const PackedQuantArgs &a, cudaStream_t st);
+// The same tokens appended behind what the sequences hold.
+cudaError_t launch_packed_extend(const PackedQuantArgs &a, cudaStream_t st);
+
+// Tokens of a paged cache read back (kivi_read.cu).
+struct ReadArgs {
+  PackedRows k, v;      // outputs
+  const int32_t *cu;    // [B + 1]
+  const int32_t *take;  // [B], null: as many as there is room for
+  const int32_t *bt;
+  const int32_t *seq_lens;
+  const uint16_t *k_res, *v_res;  // v_res null without a value residual
+  const uint32_t *k_codes, *k_meta, *v_codes, *v_meta;
+  int64_t num_pages;
+  int B, Hkv, G, bits, shift, max_pages, T;
+  int first;
+};
+cudaError_t launch_paged_read(const ReadArgs &a, cudaStream_t st);
 
 // Pages of a paged cache handed out, shared, copied, given back and moved
 // (kivi_pages.cu).  A page is free when its reference count is not positive; a table
@@ -255,6 +272,7 @@ struct PoolArgs {
   int32_t *refs;       // [num_pages]
   int32_t *info;       // [4]
   const int32_t *arg;  // reserve: extra tokens [B]; reorder: parent [B]
+  int window, sinks;   // reserve: the window that the tokens to come have (0: the whole context)
   int32_t *new_ids;    // compact: [num_pages]
   void *ws;
   int num_pages;

@@ -33,17 +33,39 @@ constexpr int kQUnit = 64, kQThreads = 128;
 static_assert(kPackedMaxSeqs == kPagedMaxBatch, "a packed batch is a paged batch");
 constexpr int kQCtas = 7;  // CTAs that fit on an SM (registers): a launch is one wave of them
 
-// Where a run of units stands.
+// Where a run of units stands.  EXT: the new tokens stand behind what the sequences hold; the units
+// are those of 64 positions that hold a new one.
+template <bool EXT>
 struct UnitWalk {
   const int32_t *cu;
   int n_seqs, T, cap;
   int seq, start, len, t0;  // sequence, its first row, its tokens (cut to the capacity), the unit's first
+  const int32_t *lens;      // EXT: tokens that the sequences hold
+  int old;                  // of `seq`
 
+  // First row of sequence s, its tokens with the new ones, those before (0 without new ones).
+  __device__ __forceinline__ void bounds(int s, int *a, int *n, int *before) const {
+    packed_bounds(cu, s, T, a, n);
+    *before = 0;
+    if constexpr (EXT) {
+      const int o = min(max(lens[s], 0), cap);
+      if (*n == 0 || o == cap) {
+        *n = 0;
+      } else {
+        *before = o;
+        *n = (int)min((int64_t)o + *n, (int64_t)cap);
+      }
+    } else {
+      *n = min(*n, cap);
+    }
+  }
+  static __device__ __forceinline__ int units(int n, int before) {
+    return EXT ? (n - before / kQUnit * kQUnit + kQUnit - 1) / kQUnit : (n + kQUnit - 1) / kQUnit;
+  }
   __device__ __forceinline__ void at(int s) {
     seq = s;
-    packed_bounds(cu, s, T, &start, &len);
-    len = min(len, cap);
-    t0 = 0;
+    bounds(s, &start, &len, &old);
+    t0 = EXT ? old / kQUnit * kQUnit : 0;
   }
   // The next unit; there is one.
   __device__ __forceinline__ void next() {
@@ -58,9 +80,9 @@ struct UnitWalk {
     for (int k = 0; k < per; ++k) {
       const int s = lane * per + k;
       if (s < n_seqs) {
-        int a, m;
-        packed_bounds(cu, s, T, &a, &m);
-        sum += (min(m, cap) + kQUnit - 1) / kQUnit;
+        int a, m, o;
+        bounds(s, &a, &m, &o);
+        sum += units(m, o);
       }
     }
     *mine = sum;
@@ -72,7 +94,7 @@ struct UnitWalk {
     }
     *incl = in;
     // bounds that overlap can pass any count: cut at what lengths that do not overlap can reach
-    return min((int64_t)T / kQUnit + n_seqs, (int64_t)max(__shfl_sync(0xffffffffu, in, 31), 0));
+    return min((int64_t)T / kQUnit + (EXT ? 2 : 1) * n_seqs, (int64_t)max(__shfl_sync(0xffffffffu, in, 31), 0));
   }
   // To unit `idx` < begin(): a scan over the warp finds the lane, its sequences the unit.
   __device__ __forceinline__ void find(int64_t idx, int incl, int mine) {
@@ -82,11 +104,11 @@ struct UnitWalk {
     int rest = (int)(idx - __shfl_sync(0xffffffffu, incl - mine, owner));
     int s = owner * per;
     at(min(s, n_seqs - 1));
-    while (rest >= (len + kQUnit - 1) / kQUnit && seq + 1 < n_seqs) {
-      rest -= (len + kQUnit - 1) / kQUnit;
+    while (rest >= units(len, old) && seq + 1 < n_seqs) {
+      rest -= units(len, old);
       at(seq + 1);
     }
-    t0 = rest * kQUnit;
+    t0 += rest * kQUnit;
   }
 };
 
@@ -110,13 +132,16 @@ __device__ __forceinline__ uint32_t codes2_counted(const uint32_t x[4], const ui
   return (w & 0x3333u) | ((w >> 14) & 0xccccu);
 }
 
-template <int BITS>
+// EXT: the tokens are appended.  The rows of a sequence's last group that lie in its residual are read
+// from there.  What fills no group goes to the residual with the sequence's first unit, by the CTA that
+// has just read the residual, and the lengths change behind this kernel, which other CTAs read.
+template <int BITS, bool EXT>
 __global__ void __launch_bounds__(kQThreads, kQCtas) packed_quantize_kernel(const PackedQuantArgs a) {
   constexpr int WPR = words_per_row<BITS>();
   __shared__ uint2 s_mm[kQThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = a.G;
-  UnitWalk u = {a.cu, a.B, a.T, a.max_pages << a.shift, 0, 0, 0, 0};
+  UnitWalk<EXT> u = {a.cu, a.B, a.T, a.max_pages << a.shift, 0, 0, 0, 0, a.seq_lens, 0};
   int incl, mine;
   const int64_t items = u.begin(&incl, &mine) * a.Hkv * 2;  // keys and values of a unit apart
   const int64_t first = items * blockIdx.x / gridDim.x, end = items * (blockIdx.x + 1) / gridDim.x;
@@ -134,16 +159,42 @@ __global__ void __launch_bounds__(kQThreads, kQCtas) packed_quantize_kernel(cons
     if ((unsigned)t0 >= (unsigned)n) return;  // only where bounds overlap
     const int nq = n / G * G, rows = min(kQUnit, n - t0);
     const int nv = a.v_res ? nq : n;  // values quantized token by token
-    if (keys && t0 == 0 && h == 0 && tid == 0) a.seq_lens[b] = n;
-    const uint16_t *ks = a.k.p + (int64_t)(u.start + t0) * a.k.ts + (int64_t)h * a.k.hs;
-    const uint16_t *vs = a.v.p + (int64_t)(u.start + t0) * a.v.ts + (int64_t)h * a.v.hs;
+    if (!EXT && keys && t0 == 0 && h == 0 && tid == 0) a.seq_lens[b] = n;
+    // rows of the unit from `fresh` on are new, those from `kept` on before it in the residual (EXT)
+    const int fresh = EXT ? u.old - t0 : 0, kept = EXT ? u.old / G * G - t0 : 0;
+    const int64_t row_in = EXT ? (int64_t)u.start - fresh : (int64_t)(u.start + t0);  // of the unit's first row
+    const uint16_t *ks = a.k.p + row_in * a.k.ts + (int64_t)h * a.k.hs;
+    const uint16_t *vs = a.v.p + row_in * a.v.ts + (int64_t)h * a.v.hs;
+    // Chunk c of row `row` of the unit: zeros where there is none.
+    auto chunk = [&](const uint16_t *src, int64_t ts, const uint16_t *res, int row, int c) {
+      if (!EXT) return row < rows ? __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)row * ts) + c) : make_uint4(0u, 0u, 0u, 0u);
+      if (row >= rows) return make_uint4(0u, 0u, 0u, 0u);
+      if (row >= fresh) return __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)row * ts) + c);
+      if (!res || row < kept) return make_uint4(0u, 0u, 0u, 0u);
+      return *(reinterpret_cast<const uint4 *>(res + (((int64_t)b * a.Hkv + h) * G + row - kept) * kD) + c);
+    };
     const int64_t page = a.bt[(int64_t)b * a.max_pages + (t0 >> a.shift)];
     const bool paged = page >= 0 && page < a.num_pages;
     // first row of the unit in the pool (the first page when the table gives none: not written)
     const int64_t row0 = (((paged ? page : 0) * a.Hkv + h) << a.shift) + (t0 & ((1 << a.shift) - 1));
 
-    // What fills no group stays in fp16: rows nq .. n - 1 that lie in this unit.
+    // What fills no group stays in fp16: rows nq .. n - 1, of this unit; the new ones of them, of the
+    // sequence (EXT).
     auto keep = [&](const uint16_t *src, int64_t ts, uint16_t *dst) {
+      if constexpr (EXT) {
+        if (t0 != u.old / kQUnit * kQUnit) return;
+        __syncthreads();  // the CTA has read the residual
+        const int first = max(nq, u.old);
+        if (first >= n) return;
+        const int64_t last = a.bt[(int64_t)b * a.max_pages + (nq >> a.shift)];  // tokens without a page are dropped
+        if (last < 0 || last >= a.num_pages) return;
+        for (int it = tid; it < (n - first) * (kD / 8); it += kQThreads) {
+          const int r = first + it / (kD / 8), c = it % (kD / 8);
+          *reinterpret_cast<uint4 *>(dst + (((int64_t)b * a.Hkv + h) * G + r - nq) * kD + 8 * c) =
+              __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)(r - t0) * ts) + c);
+        }
+        return;
+      }
       for (int it = tid; it < kQUnit * (kD / 8); it += kQThreads) {
         const int r = it / (kD / 8), c = it % (kD / 8);
         if (t0 + r < nq || r >= rows) continue;
@@ -157,8 +208,7 @@ __global__ void __launch_bounds__(kQThreads, kQCtas) packed_quantize_kernel(cons
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int row = 32 * rh + t4 + 4 * k;
-        const uint4 c = row < rows ? __ldg(reinterpret_cast<const uint4 *>(ks + (int64_t)row * a.k.ts) + 8 * ch + c8)
-                                   : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 c = chunk(ks, a.k.ts, a.k_res, row, 8 * ch + c8);
         x[k][0] = c.x;
         x[k][1] = c.y;
         x[k][2] = c.z;
@@ -197,7 +247,7 @@ __global__ void __launch_bounds__(kQThreads, kQCtas) packed_quantize_kernel(cons
         pmx = __hmax2(pmx, u2h2(o.y));
       }
       const int g0 = G == 32 ? 32 * rh : 0;           // first row of the warp's group in the unit
-      if (paged && t0 + g0 + G <= nq) {               // a quantized group (not the residual)
+      if (paged && t0 + g0 + G <= nq && (!EXT || g0 >= kept)) {  // a quantized group (not the residual)
         const QParams p0 = make_qparams<BITS>(__low2float(pmn), __low2float(pmx));
         const QParams p1 = make_qparams<BITS>(__high2float(pmn), __high2float(pmx));
         if (G == 32 || rh == 0)
@@ -273,7 +323,7 @@ __global__ void __launch_bounds__(kQThreads, kQCtas) packed_quantize_kernel(cons
           }
         }
       }
-      if (t0 + rows > nq) keep(ks, a.k.ts, a.k_res);
+      if (EXT || t0 + rows > nq) keep(ks, a.k.ts, a.k_res);
     } else {
       const int q = lane & 3;
       uint4 y[2][4];
@@ -282,14 +332,13 @@ __global__ void __launch_bounds__(kQThreads, kQCtas) packed_quantize_kernel(cons
         const int row = 32 * i + 8 * warp + (lane >> 2);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          y[i][k] = row < rows ? __ldg(reinterpret_cast<const uint4 *>(vs + (int64_t)row * a.v.ts) + q + 4 * k)
-                               : make_uint4(0u, 0u, 0u, 0u);
+          y[i][k] = chunk(vs, a.v.ts, a.v_res, row, q + 4 * k);
       }
       // ---- value rows: lane q of a row holds chunks q + 4k (8 channels each)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = 32 * i + 8 * warp + (lane >> 2);
-        const bool ok_row = paged && t0 + r < nv;
+        const bool ok_row = paged && t0 + r < nv && (!EXT || r >= (a.v_res ? kept : fresh));
         __half2 vmn = u2h2(y[i][0].x), vmx = vmn;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -346,24 +395,54 @@ __global__ void __launch_bounds__(kQThreads, kQCtas) packed_quantize_kernel(cons
         }
         if (ok_row && q == 0) a.v_meta[row0 + r] = p.meta;
       }
-      if (a.v_res && t0 + rows > nq) keep(vs, a.v.ts, a.v_res);
+      if (a.v_res && (EXT || t0 + rows > nq)) keep(vs, a.v.ts, a.v_res);
     }
   }
 }
 
-}  // namespace
+// The sequences' new lengths, behind the quantizer.
+__global__ void __launch_bounds__(kPackedMaxSeqs) extend_lens_kernel(const PackedQuantArgs a) {
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const int s = threadIdx.x;
+  if (s >= a.B) return;
+  const UnitWalk<true> u = {a.cu, a.B, a.T, a.max_pages << a.shift, 0, 0, 0, 0, a.seq_lens, 0};
+  int start, n, before;
+  u.bounds(s, &start, &n, &before);
+  if (n > 0) a.seq_lens[s] = n;
+}
 
-cudaError_t launch_packed_quantize(const PackedQuantArgs &a, cudaStream_t st) {
+// One wave of CTAs, or fewer where there is less work.
+template <bool EXT>
+cudaError_t launch_quantizer(const PackedQuantArgs &a, cudaStream_t st) {
   int sms = 0;
   const cudaError_t e = device_sms(&sms);
   if (e != cudaSuccess) return e;
-  const int64_t items = ((int64_t)a.T / kQUnit + a.B) * a.Hkv * 2, wave = (int64_t)sms * kQCtas;
+  const int64_t items = ((int64_t)a.T / kQUnit + (EXT ? 2 : 1) * a.B) * a.Hkv * 2, wave = (int64_t)sms * kQCtas;
   const unsigned grid = (unsigned)(items < wave ? items : wave);
   if (a.bits == 2)
-    packed_quantize_kernel<2><<<grid, kQThreads, 0, st>>>(a);
+    packed_quantize_kernel<2, EXT><<<grid, kQThreads, 0, st>>>(a);
   else
-    packed_quantize_kernel<4><<<grid, kQThreads, 0, st>>>(a);
+    packed_quantize_kernel<4, EXT><<<grid, kQThreads, 0, st>>>(a);
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_packed_quantize(const PackedQuantArgs &a, cudaStream_t st) { return launch_quantizer<false>(a, st); }
+
+cudaError_t launch_packed_extend(const PackedQuantArgs &a, cudaStream_t st) {
+  const cudaError_t e = launch_quantizer<true>(a, st);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kPackedMaxSeqs);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, extend_lens_kernel, a);
 }
 
 }  // namespace kivi

@@ -191,11 +191,23 @@ __device__ __forceinline__ bool in_pool(const PoolArgs &a, int page) { return pa
 __device__ __forceinline__ int clamp_len(const PoolArgs &a, int n) { return min(max(n, 0), a.max_pages << a.shift); }
 
 // ------------------------------------------------------------------------- reserve
+// Table entries [a, b) of a sequence whose positions no token to come sees, nor any behind: outside the
+// window of the next one, and no sinks.
+__device__ __forceinline__ void unseen_entries(const PoolArgs &a, int len, int *from, int *to) {
+  const int P = 1 << a.shift;
+  *from = a.sinks / P + (a.sinks % P != 0);
+  *to = max(*from, max(clamp_len(a, len) - a.window + 1, 0) / P);
+}
+
+// WIN: pages out of the window's reach are given back first, and get no successor.
+template <bool WIN>
 __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads)
     pool_reserve_kernel(const PoolArgs a, const Ws ws) {
   __shared__ Shared sh;
   __shared__ int s_rank[64];  // missing entries of this CTA's rows, then the rank of each row's first
+  __shared__ int s_freed;     // WIN, of the first CTA: pages given back
   cg::cluster_group cl = cg::this_cluster();
+  if (WIN && threadIdx.x == 0) s_freed = 0;
   cl.barrier_arrive();  // this CTA runs: see exchange()
   const int r = (int)cl.block_rank(), lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int per = (a.B + kPoolCtas - 1) / kPoolCtas;  // <= 64
@@ -207,14 +219,36 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
     const int64_t want = min(cap, (int64_t)max(a.seq_lens[b], 0) + extra);
     return (int)((want + (1 << a.shift) - 1) >> a.shift);
   };
+  int gone = 0;  // pages that this warp's rows gave back
   for (int i = w; i < rows; i += kPoolWarps) {
     const int m = entries(b0 + i);
-    const int32_t *row = a.bt + (int64_t)(b0 + i) * a.max_pages;
+    int32_t *row = a.bt + (int64_t)(b0 + i) * a.max_pages;
     int c = 0;
+    if constexpr (WIN) {
+      int from = 0, to = 0;
+      if (m > 0) unseen_entries(a, a.seq_lens[b0 + i], &from, &to);
 #pragma unroll 4
-    for (int j = lane; j < m; j += 32) c += !in_pool(a, row[j]);
+      for (int j = lane; j < m; j += 32) c += !in_pool(a, row[j]) && !(j >= from && j < to);
+      int freed = 0;
+      for (int j = from + lane; j < to; j += 32) {
+        const int page = row[j];
+        if (page == -1) continue;
+        row[j] = -1;
+        if (in_pool(a, page)) freed += atomicAdd(a.refs + page, -1) == 1;
+      }
+      freed = __reduce_add_sync(0xffffffffu, freed);
+      if (lane == 0 && freed) gone += freed;
+    } else {
+#pragma unroll 4
+      for (int j = lane; j < m; j += 32) c += !in_pool(a, row[j]);
+    }
     c = __reduce_add_sync(0xffffffffu, c);
     if (lane == 0) s_rank[i] = c;
+  }
+  if constexpr (WIN) {
+    cl.barrier_wait();  // every CTA runs
+    if (gone) atomicAdd(cl.map_shared_rank(&s_freed, 0), gone);
+    cl.sync();          // every page that goes is counted out
   }
   int lo, hi;
   slice(r, a.num_pages, &lo, &hi);
@@ -223,7 +257,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   int missing;
   const int before = block_scan((int)threadIdx.x < rows ? s_rank[threadIdx.x] : 0, sh, &missing);
   Spread fr, ms;
-  cl.barrier_wait();  // every CTA runs
+  if constexpr (!WIN) cl.barrier_wait();  // every CTA runs
   exchange(cl, sh, nfree, missing, &fr, &ms);
   if ((int)threadIdx.x < rows) s_rank[threadIdx.x] = ms.before + before;
   const int got = min(fr.all, ms.all);
@@ -236,16 +270,19 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
     const int m = entries(b0 + i);
     int32_t *row = a.bt + (int64_t)(b0 + i) * a.max_pages;
     int k = s_rank[i];
+    int from = 0, to = 0;
+    if (WIN && m > 0) unseen_entries(a, a.seq_lens[b0 + i], &from, &to);
     for (int j0 = 0; j0 < m; j0 += 128) {  // four loads in flight
       int page[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) page[u] = j0 + 32 * u + lane < m ? row[j0 + 32 * u + lane] : 0;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const bool want = !in_pool(a, page[u]);  // page 0 past the end is one
+        const int j = j0 + 32 * u + lane;
+        const bool want = !in_pool(a, page[u]) && !(WIN && j >= from && j < to);  // page 0 past the end is one
         const uint32_t mask = __ballot_sync(0xffffffffu, want);
         const int mine = k + __popc(mask & ((1u << lane) - 1u));
-        if (want) row[j0 + 32 * u + lane] = mine < got ? __ldcg(ws.list + mine) : -1;
+        if (want) row[j] = mine < got ? __ldcg(ws.list + mine) : -1;
         k += __popc(mask);
       }
     }
@@ -254,7 +291,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
     a.info[0] = got;
     a.info[1] = ms.all - got;
     a.info[2] = a.num_pages - fr.all + got;
-    a.info[3] = 0;
+    a.info[3] = WIN ? s_freed : 0;
   }
 }
 
@@ -553,7 +590,10 @@ size_t pool_workspace_bytes(int B, int Hkv, int G, int max_pages, int64_t num_pa
 }
 
 cudaError_t launch_pool_reserve(const PoolArgs &a, cudaStream_t st) {
-  pool_reserve_kernel<<<kPoolCtas, kPoolThreads, 0, st>>>(a, workspace_of(a));
+  if (a.window)
+    pool_reserve_kernel<true><<<kPoolCtas, kPoolThreads, 0, st>>>(a, workspace_of(a));
+  else
+    pool_reserve_kernel<false><<<kPoolCtas, kPoolThreads, 0, st>>>(a, workspace_of(a));
   return cudaGetLastError();
 }
 

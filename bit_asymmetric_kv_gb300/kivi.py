@@ -111,11 +111,16 @@ def lib() -> ctypes.CDLL:
         L.kivi_prefill_attention_window.argtypes = [i32, i32, i32, i32, P, i64, P, i64, PR, PR, PR, ctypes.c_float, i32,
                                                     i32, PR, P]
         L.kivi_paged_prefill_packed.argtypes = [PD, PC, P, i64, PR, PR, P]
+        L.kivi_paged_extend_packed.argtypes = [PD, PC, P, i64, PR, PR, P]
+        L.kivi_paged_read.argtypes = [PD, PC, P, i64, P, i32, PR, PR, P]
         L.kivi_paged_pool_workspace_bytes.argtypes = [PD]
         L.kivi_paged_pool_workspace_bytes.restype = sz
         for name in ("kivi_paged_reserve", "kivi_paged_reorder", "kivi_paged_compact"):
             getattr(L, name).argtypes = [PD, PC, PP, P, P, sz, P]
-        for name in ("kivi_prefill_attention_packed", "kivi_prefill_attention_window", "kivi_paged_prefill_packed", "kivi_paged_reserve",
+        L.kivi_paged_reserve_window.argtypes = [PD, PC, PP, P, i32, i32, P, sz, P]
+        L.kivi_paged_reserve_window.restype = ctypes.c_int
+        for name in ("kivi_prefill_attention_packed", "kivi_prefill_attention_window", "kivi_paged_prefill_packed",
+                     "kivi_paged_extend_packed", "kivi_paged_read", "kivi_paged_reserve",
                      "kivi_paged_reorder", "kivi_paged_compact"):
             getattr(L, name).restype = ctypes.c_int
         L.kivi_status_string.argtypes = [ctypes.c_int]
@@ -616,13 +621,39 @@ def kivi_paged_prefill_packed(cache: PagedCache, k: torch.Tensor, v: torch.Tenso
                               stream=None) -> None:
     """Prompts of all sequences of a paged batch, packed: k, v fp16 [T, Hkv, D] (strides as for
     kivi_prefill_attention_packed), cu_seqlens int32 [B + 1]; an empty sequence is left as it is."""
-    d, dev = cache.dims, cache.k_codes.device
-    rk, rv = _rows(k, "k", dev), _rows(v, "v", dev)
-    if k.shape != v.shape or tuple(k.shape[1:]) != (d.Hkv, d.D):
-        raise ValueError(f"k {list(k.shape)}, v {list(v.shape)}: expected [tokens, {d.Hkv}, {d.D}]")
-    cu = _i32(cu_seqlens, "cu_seqlens", d.B + 1, dev)
+    dev, cu, rk, rv = _pack(cache, cu_seqlens, k, v, "k", "v")
     if k.shape[0]:
-        _run("kivi_paged_prefill_packed", dev, stream, d, cache.c, cu, k.shape[0], rk, rv)
+        _run("kivi_paged_prefill_packed", dev, stream, cache.dims, cache.c, cu, k.shape[0], rk, rv)
+
+
+def _pack(cache: PagedCache, cu_seqlens: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_name: str, v_name: str):
+    """(device, bounds, rows of k, rows of v) of a paged batch's packed keys and values."""
+    d, dev = cache.dims, cache.k_codes.device
+    rk, rv = _rows(k, k_name, dev), _rows(v, v_name, dev)
+    if k.shape != v.shape or tuple(k.shape[1:]) != (d.Hkv, d.D):
+        raise ValueError(f"{k_name} {list(k.shape)}, {v_name} {list(v.shape)}: expected [tokens, {d.Hkv}, {d.D}]")
+    return dev, _i32(cu_seqlens, "cu_seqlens", d.B + 1, dev), rk, rv
+
+
+def kivi_paged_extend_packed(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                             stream=None) -> None:
+    """New tokens of all sequences of a paged batch, packed, behind what the sequences hold: k, v fp16
+    [T, Hkv, D] (strides as for kivi_prefill_attention_packed), cu_seqlens int32 [B + 1]; the lengths grow."""
+    dev, cu, rk, rv = _pack(cache, cu_seqlens, k, v, "k", "v")
+    if k.shape[0]:
+        _run("kivi_paged_extend_packed", dev, stream, cache.dims, cache.c, cu, k.shape[0], rk, rv)
+
+
+def kivi_paged_read(cache: PagedCache, cu_seqlens: torch.Tensor, take: torch.Tensor | None, k_out: torch.Tensor,
+                    v_out: torch.Tensor, first: int = 0, stream=None) -> None:
+    """The first `first` and the newest tokens of every sequence, take[s] of them together (int32 [B] on the
+    device; None: as many as it has rows), as fp16 rows cu_seqlens[s] .. of k_out and v_out [T, Hkv, D] (strides
+    as for kivi_prefill_attention_packed); the rows behind them are left as they were."""
+    dev, cu, rk, rv = _pack(cache, cu_seqlens, k_out, v_out, "k_out", "v_out")
+    at = None if take is None else _i32(take, "take", cache.dims.B, dev)
+    first = _count(first, "first", 0)
+    if k_out.shape[0]:
+        _run("kivi_paged_read", dev, stream, cache.dims, cache.c, cu, k_out.shape[0], at, first, rk, rv)
 
 
 def kivi_paged_pool_workspace_bytes(dims: kivi_paged_dims) -> int:
@@ -672,6 +703,16 @@ def _pool_call(name: str, cache: PagedCache, pool: PagePool, array: torch.Tensor
 def kivi_paged_reserve(cache: PagedCache, pool: PagePool, extra: torch.Tensor, stream=None) -> None:
     """Pages for extra[b] more tokens of every sequence b (int32 [B] on the device; <= 0: none)."""
     _pool_call("kivi_paged_reserve", cache, pool, extra, "extra", cache.dims.B, stream)
+
+
+def kivi_paged_reserve_window(cache: PagedCache, pool: PagePool, extra: torch.Tensor, window: int, sinks: int,
+                              stream=None) -> None:
+    """kivi_paged_reserve for attention with a sliding window and sinks: of the sequences with extra[b] > 0, pages
+    that no token to come sees are given back first, and their table entries get none."""
+    dev = cache.k_codes.device
+    at = _i32(extra, "extra", cache.dims.B, dev)
+    _run("kivi_paged_reserve_window", dev, stream, cache.dims, cache.c, pool.c, at, _count(window, "window", 1),
+         _count(sinks, "sinks", 0), pool.ws.data_ptr(), pool.ws.numel())
 
 
 def kivi_paged_reorder(cache: PagedCache, pool: PagePool, parent: torch.Tensor, stream=None) -> None:

@@ -479,6 +479,34 @@ KIVI_API int kivi_paged_prefill_packed(const kivi_paged_dims *dims, const kivi_p
                                        const kivi_rows *v, cudaStream_t stream);
 
 /*
+ * Append the packed tokens of a paged batch behind what its sequences hold: row i of sequence s of the pack
+ * becomes position seq_lens[s] + i of sequence s of the cache (n_seqs = dims->B), written as
+ * kivi_paged_append_token writes one token after the other: codes, scales, zeros and residual bit for bit.  The
+ * key groups that fill are quantized, the first from the residual and the new keys; then seq_lens[s] grows
+ * by the sequence's rows.  A sequence without rows is left as it is.  Tokens at or beyond max_pages_per_seq *
+ * P are dropped, and so are those of a position whose table entry lies outside the pool (the length still
+ * counts the latter).  Assign pages first (kivi_paged_reserve, kivi_paged_reserve_window).
+ */
+KIVI_API int kivi_paged_extend_packed(const kivi_paged_dims *dims, const kivi_paged_cache *cache,
+                                      const int32_t *cu_seqlens, int64_t n_tokens, const kivi_rows *k,
+                                      const kivi_rows *v, cudaStream_t stream);
+
+/*
+ * Read tokens of a paged batch back as fp16 rows, for attention over earlier tokens and new ones side by
+ * side (kivi_prefill_attention_window).  Sequence s has the rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 of k_out and
+ * v_out (n_tokens rows, Hkv heads).  Of its n tokens, c = min(take[s], n, its rows) are read (take: int32 [B] on
+ * the device, at most 0 reads none; NULL: as many as it has rows): the first min(first, c), then the newest ones,
+ * in order; its row i is position i for i < first, else position n - c + i.  With take[s] = its rows less those of
+ * the next chunk, the chunk's own keys and values have their place behind them.  Rows behind the c are left as
+ * they were.  An element is fp16(z + code * s) of the exact product and sum, rounded once, at most 65504 in
+ * magnitude; residual tokens are copied; a position whose table entry lies outside the pool reads as
+ * zeros.  Elements of k_out and v_out must not overlap one another (KIVI_ERR_ARG within each).
+ */
+KIVI_API int kivi_paged_read(const kivi_paged_dims *dims, const kivi_paged_cache *cache, const int32_t *cu_seqlens,
+                             int64_t n_tokens, const int32_t *take, int32_t first, const kivi_rows *k_out,
+                             const kivi_rows *v_out, cudaStream_t stream);
+
+/*
  * ---- Pages handed out on the device ----------------------------------------------------
  * A caller may assign pages itself, or leave it to the three calls below.  They keep one
  * reference count per page beside the block table: a page is free when its count is not
@@ -511,6 +539,20 @@ KIVI_API size_t kivi_paged_pool_workspace_bytes(const kivi_paged_dims *dims);
 KIVI_API int kivi_paged_reserve(const kivi_paged_dims *dims, const kivi_paged_cache *cache,
                                 const kivi_page_pool *pool, const int32_t *extra, void *ws, size_t ws_bytes,
                                 cudaStream_t stream);
+
+/*
+ * kivi_paged_reserve for sequences whose attention has a sliding window and sinks: in every sequence b with
+ * extra[b] > 0, the table entries whose positions no token to come sees (every position before
+ * seq_lens[b] - window + 1 and at or beyond `sinks`) first give their pages back: the page's count falls by
+ * one and the entry becomes -1.  Pages that are free then are handed out in the same call, to the other entries of
+ * positions 0 .. seq_lens[b] + extra[b] - 1 that hold none.  Where the chunk's attention reads earlier tokens back
+ * (kivi_paged_read), those that its first query sees are still there.  window >= 1, sinks >= 0
+ * (KIVI_ERR_ARG).  info = {pages handed out, pages that were not there, pages in use afterwards, pages that became
+ * free}.  (kivi_paged_reserve would give the entries out of reach new pages.)
+ */
+KIVI_API int kivi_paged_reserve_window(const kivi_paged_dims *dims, const kivi_paged_cache *cache,
+                                       const kivi_page_pool *pool, const int32_t *extra, int32_t window,
+                                       int32_t sinks, void *ws, size_t ws_bytes, cudaStream_t stream);
 
 /*
  * Fork, free and reorder sequences: afterwards sequence b is what sequence parent[b] was

@@ -140,7 +140,10 @@ def test_a_window_over_everything_is_the_whole_context():
     q = torch.randn((5, 8, D), device="cuda").to(torch.float16)
     whole = kivi.kivi_paged_decode_attention(c, q, SCALE)
     for window, sinks in ((1200, 0), (2**40, 2**40), (1, 1200)):
-        assert torch.equal(kivi.kivi_paged_decode_attention_window(c, q, window, sinks, SCALE), whole)
+        out = kivi.kivi_paged_decode_attention_window(c, q, window, sinks, SCALE).float()
+        # Both sum the same terms in fp32, in other orders, and round once to fp16: half a step, 2^-11 |out|, each.
+        # The sums: |out| < 4 here, at most 1200 terms in groups of 16, 2^-24 each: below 2^-13 in all.
+        assert ((out - whole.float()).abs() <= 2 * 2.0**-11 * whole.float().abs() + 2.0**-13).all()
 
 
 def test_long_contexts_and_many_sequences():

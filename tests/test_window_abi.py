@@ -86,6 +86,42 @@ def test_step_refuses_its_token(L):
     assert call(_dims(), _cache(), FAKE + 4, FAKE, *rest) == 2 and call(_dims(), _cache(), FAKE, FAKE + 8, *rest) == 2
 
 
+@pytest.mark.parametrize("bad,status", [
+    (dict(dims=_dims(B=0)), 1), (dict(dims=_dims(G=48)), 3), (dict(dims=_dims(value_residual=1)), 1),
+    (dict(cache=_cache(table=0)), 1), (dict(cu=0), 1), (dict(cu=FAKE + 1), 2), (dict(T=-1), 1), (dict(T=1 << 31), 3),
+    (dict(k=_rows(0)), 1), (dict(v=_rows(FAKE + 2)), 2), (dict(k=_rows(ts=4)), 1), (dict(v=_rows(hs=129)), 2),
+])
+def test_extend_and_read_refuse(L, bad, status):
+    a = dict(dims=_dims(), cache=_cache(), cu=FAKE, T=10, k=_rows(), v=_rows())
+    a.update(bad)
+    assert L.kivi_paged_extend_packed(a["dims"], a["cache"], a["cu"], a["T"], a["k"], a["v"], 0) == status
+    for take in (0, FAKE):
+        assert L.kivi_paged_read(a["dims"], a["cache"], a["cu"], a["T"], take, 4, a["k"], a["v"], 0) == status
+
+
+def test_read_refuses(L):
+    def call(take=FAKE, first=0, k=_rows(), v=_rows(), T=10):
+        return L.kivi_paged_read(_dims(), _cache(), FAKE, T, take, first, k, v, 0)
+
+    assert call(take=FAKE + 2) == 2 and call(first=-1) == 1
+    assert call(k=_rows(ts=128, hs=128)) == 1 and call(v=_rows(ts=128, hs=9 * 128)) == 1  # elements on one another
+    assert call(T=0) == 0 and L.kivi_paged_extend_packed(_dims(), _cache(), FAKE, 0, _rows(), _rows(), 0) == 0
+
+
+def test_reserve_window_refuses(L):
+    dims, ws = _dims(), kivi.kivi_paged_pool_workspace_bytes(_dims())
+
+    def call(dims=dims, table=FAKE, refs=FAKE, info=FAKE, extra=FAKE, window=5, sinks=1, at=FAKE, nbytes=ws):
+        pool = kivi.kivi_page_pool(table, refs, info)
+        return L.kivi_paged_reserve_window(dims, _cache(), pool, extra, window, sinks, at, nbytes, 0)
+
+    assert call(window=0) == 1 and call(window=-1) == 1 and call(sinks=-1) == 1
+    assert call(dims=_dims(Hkv=0)) == 1 and call(dims=_dims(bits=3)) == 3 and call(table=FAKE + 4096) == 1
+    assert call(refs=0) == 1 and call(info=0) == 1 and call(extra=0) == 1
+    assert call(refs=FAKE + 4) == 2 and call(extra=FAKE + 2) == 2
+    assert call(at=0) == 5 and call(nbytes=ws - 1) == 5 and call(at=FAKE + 8) == 2
+
+
 def test_binding_refuses(L):
     half = torch.zeros((4, 2, 128), dtype=torch.float16)
     cu = torch.tensor([0, 4], dtype=torch.int32)
