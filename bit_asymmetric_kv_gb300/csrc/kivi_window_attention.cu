@@ -45,6 +45,86 @@ constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "more registers than the CTA was launched with");
 constexpr int kStages = 4;                  // K and V tiles in flight
 
+// All sequences' blocks, those whose last row stands at the highest position first: a block's passes
+// never grow as its position falls, so that long and short blocks are dealt out evenly whatever the
+// sequences' queries and keys.  Block L of sequence s has the order lead_s + L, in blocks of
+// positions; block `item` is found by a binary search for its order and a count over the sequences.
+// Kept in shared memory, built once by a CTA.
+struct WindowList {
+  int qrow[kPackedMaxSeqs], len[kPackedMaxSeqs], krow[kPackedMaxSeqs], keys[kPackedMaxSeqs];
+  int lead[kPackedMaxSeqs], nb[kPackedMaxSeqs];
+  int n, lo, hi;  // sequences; the lowest and highest order
+  int total;
+
+  // Every thread of the CTA calls it; synchronises.
+  __device__ __forceinline__ void build(const WindowAttentionArgs &a, int bt) {
+    for (int s = threadIdx.x; s < a.n_seqs; s += blockDim.x) {
+      int r, m, kr, km;
+      packed_bounds(a.cu, s, a.T, &r, &m);
+      packed_bounds(a.cu_kv, s, a.Tk, &kr, &km);
+      qrow[s] = r;
+      len[s] = m;
+      krow[s] = kr;
+      keys[s] = km;
+      nb[s] = m / bt + (m % bt != 0);
+      lead[s] = km > m ? (km - m) / bt : 0;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      int64_t sum = 0;
+      int x = 0x7fffffff, y = 0;
+      for (int s = threadIdx.x; s < a.n_seqs; s += 32)
+        if (nb[s]) {
+          sum += nb[s];
+          x = min(x, lead[s]);
+          y = max(y, lead[s] + nb[s] - 1);
+        }
+#pragma unroll
+      for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      x = __reduce_min_sync(0xffffffffu, x);
+      y = __reduce_max_sync(0xffffffffu, y);
+      if (threadIdx.x == 0) {
+        n = a.n_seqs;
+        lo = x;
+        hi = y;
+        // bounds that overlap may pass any count: cut at what lengths that do not overlap can reach
+        total = (int)min((int64_t)a.T / bt + a.n_seqs, sum);
+      }
+    }
+    __syncthreads();
+  }
+
+  // Sequence and level of block `item` < total; every lane of a warp calls it.
+  __device__ __forceinline__ void find(unsigned item, int lane, int *seq, int *level) const {
+    auto from = [&](int order) {  // blocks of that order and higher
+      unsigned c = 0;
+      for (int s = lane; s < n; s += 32) c += (unsigned)min(nb[s], max(0, lead[s] + nb[s] - order));
+      return __reduce_add_sync(0xffffffffu, c);
+    };
+    int a = lo, b = hi;  // the highest order with more than `item` blocks from it on
+    while (a < b) {
+      const int mid = a + (b - a + 1) / 2;
+      if (from(mid) > item)
+        a = mid;
+      else
+        b = mid - 1;
+    }
+    unsigned rest = item - from(a + 1);
+    *seq = 0;
+    *level = 0;
+    for (int s0 = 0; s0 < n; s0 += 32) {
+      const int s = s0 + lane;
+      const uint32_t has = __ballot_sync(0xffffffffu, s < n && nb[s] && a >= lead[s] && a < lead[s] + nb[s]);
+      if (rest < (unsigned)__popc(has)) {
+        *seq = s0 + (int)__fns(has, 0, (int)rest + 1);
+        *level = a - lead[*seq];
+        return;
+      }
+      rest -= __popc(has);
+    }
+  }
+};
+
 // One block of work.
 struct __align__(16) Block {
   int qrow, len;          // the sequence's first query row, its queries
@@ -79,7 +159,7 @@ struct __align__(16) Bars {
   Block slot[2];
   uint32_t tmem;
   int abort;
-  PackedList list;
+  WindowList list;
 };
 constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + (int)sizeof(Bars);
 static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
@@ -127,8 +207,8 @@ __device__ __forceinline__ void plan_passes(const WindowAttentionArgs &a, int tp
   w->nt[1] = two ? w->to[1] + (own ? sinks : 0) : 0;
 }
 
-// Block k of this CTA into slot k % 2, for the warps that work on it.  The list (longest sequences'
-// last blocks first) is dealt out back and forth.  Where K and V of all heads are more than L2 holds, the
+// Block k of this CTA into slot k % 2, for the warps that work on it.  The list is dealt out back and
+// forth, so that the first CTAs do not get the longer block of every round.  Where K and V of all heads are more than L2 holds, the
 // head groups are taken in sets that fit, one set's blocks after the other's, every other set in reverse.
 __device__ __forceinline__ void block_role(const WindowAttentionArgs &a, const Cta &c, Bars &sh, int lane) {
   const int64_t G = gridDim.x;
@@ -156,13 +236,15 @@ __device__ __forceinline__ void block_role(const WindowAttentionArgs &a, const C
       unsigned item = rest / width;
       const unsigned hg = group + rest - item * width;
       if ((c.sets - 1 - set) & 1) item = total - 1 - item;
-      const PackedBlock b = sh.list.find(item);
-      w.qrow = b.start;
-      w.len = b.len;
-      packed_bounds(a.cu_kv, b.seq, a.Tk, &w.krow, &w.keys);
+      int seq, level;
+      sh.list.find(item, lane, &seq, &level);
+      w.qrow = sh.list.qrow[seq];
+      w.len = sh.list.len[seq];
+      w.krow = sh.list.krow[seq];
+      w.keys = sh.list.keys[seq];
       w.head0 = (int)hg * c.pack;
       w.kvh = w.head0 / c.heads_per_kv;
-      w.base[0] = b.level * 2 * c.tpt;
+      w.base[0] = level * 2 * c.tpt;
       w.base[1] = w.base[0] + c.tpt;
       plan_passes(a, c.tpt, &w);
     }
@@ -532,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
   }
-  sh.list.build(a.cu, a.n_seqs, a.T, 2 * cta.tpt);  // the CTA's threads together
+  sh.list.build(a, 2 * cta.tpt);  // the CTA's threads together
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
