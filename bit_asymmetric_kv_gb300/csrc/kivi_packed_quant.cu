@@ -31,7 +31,9 @@ namespace {
 constexpr int kQUnit = 64, kQThreads = 128;
 
 static_assert(kPackedMaxSeqs == kPagedMaxBatch, "a packed batch is a paged batch");
-constexpr int kQCtas = 7;  // CTAs that fit on an SM (registers): a launch is one wave of them
+// CTAs that fit on an SM (registers): a launch is one wave of them.  4-bit codes hold the parameters of
+// a chunk's channels beside its rows (32 prompts of up to 2048 tokens: 64 us at five, 66 at six, 70 at seven).
+constexpr int q_ctas(int bits) { return bits == 2 ? 7 : 5; }
 
 // Where a run of units stands.  EXT: the new tokens stand behind what the sequences hold; the units
 // are those of 64 positions that hold a new one.
@@ -133,14 +135,15 @@ __device__ __forceinline__ uint32_t codes2_counted(const uint32_t x[4], const ui
 }
 
 // EXT: the tokens are appended.  The rows of a sequence's last group that lie in its residual are read
-// from there.  What fills no group goes to the residual with the sequence's first unit, by the CTA that
-// has just read the residual, and the lengths change behind this kernel, which other CTAs read.
+// from there.  What fills no group goes there, and the lengths change, in a kernel behind this one, whose
+// CTAs read both.
 template <int BITS, bool EXT>
-__global__ void __launch_bounds__(kQThreads, kQCtas) packed_quantize_kernel(const PackedQuantArgs a) {
+__global__ void __launch_bounds__(kQThreads, q_ctas(BITS)) packed_quantize_kernel(const PackedQuantArgs a) {
   constexpr int WPR = words_per_row<BITS>();
   __shared__ uint2 s_mm[kQThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = a.G;
+  if (EXT) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // they wait for this grid's end
   UnitWalk<EXT> u = {a.cu, a.B, a.T, a.max_pages << a.shift, 0, 0, 0, 0, a.seq_lens, 0};
   int incl, mine;
   const int64_t items = u.begin(&incl, &mine) * a.Hkv * 2;  // keys and values of a unit apart
@@ -167,34 +170,20 @@ __global__ void __launch_bounds__(kQThreads, kQCtas) packed_quantize_kernel(cons
     const uint16_t *vs = a.v.p + row_in * a.v.ts + (int64_t)h * a.v.hs;
     // Chunk c of row `row` of the unit: zeros where there is none.
     auto chunk = [&](const uint16_t *src, int64_t ts, const uint16_t *res, int row, int c) {
-      if (!EXT) return row < rows ? __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)row * ts) + c) : make_uint4(0u, 0u, 0u, 0u);
-      if (row >= rows) return make_uint4(0u, 0u, 0u, 0u);
-      if (row >= fresh) return __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)row * ts) + c);
-      if (!res || row < kept) return make_uint4(0u, 0u, 0u, 0u);
-      return *(reinterpret_cast<const uint4 *>(res + (((int64_t)b * a.Hkv + h) * G + row - kept) * kD) + c);
+      if constexpr (EXT) {
+        const uint16_t *p = row >= fresh ? src + (int64_t)row * ts : res + (((int64_t)b * a.Hkv + h) * G + row - kept) * kD;
+        return row < rows && row >= (res ? kept : fresh) ? *(reinterpret_cast<const uint4 *>(p) + c) : make_uint4(0u, 0u, 0u, 0u);
+      } else {
+        return row < rows ? __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)row * ts) + c) : make_uint4(0u, 0u, 0u, 0u);
+      }
     };
     const int64_t page = a.bt[(int64_t)b * a.max_pages + (t0 >> a.shift)];
     const bool paged = page >= 0 && page < a.num_pages;
     // first row of the unit in the pool (the first page when the table gives none: not written)
     const int64_t row0 = (((paged ? page : 0) * a.Hkv + h) << a.shift) + (t0 & ((1 << a.shift) - 1));
 
-    // What fills no group stays in fp16: rows nq .. n - 1, of this unit; the new ones of them, of the
-    // sequence (EXT).
+    // What fills no group stays in fp16: rows nq .. n - 1 that lie in this unit.
     auto keep = [&](const uint16_t *src, int64_t ts, uint16_t *dst) {
-      if constexpr (EXT) {
-        if (t0 != u.old / kQUnit * kQUnit) return;
-        __syncthreads();  // the CTA has read the residual
-        const int first = max(nq, u.old);
-        if (first >= n) return;
-        const int64_t last = a.bt[(int64_t)b * a.max_pages + (nq >> a.shift)];  // tokens without a page are dropped
-        if (last < 0 || last >= a.num_pages) return;
-        for (int it = tid; it < (n - first) * (kD / 8); it += kQThreads) {
-          const int r = first + it / (kD / 8), c = it % (kD / 8);
-          *reinterpret_cast<uint4 *>(dst + (((int64_t)b * a.Hkv + h) * G + r - nq) * kD + 8 * c) =
-              __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)(r - t0) * ts) + c);
-        }
-        return;
-      }
       for (int it = tid; it < kQUnit * (kD / 8); it += kQThreads) {
         const int r = it / (kD / 8), c = it % (kD / 8);
         if (t0 + r < nq || r >= rows) continue;
@@ -267,12 +256,7 @@ __global__ void __launch_bounds__(kQThreads, kQCtas) packed_quantize_kernel(cons
           }
           // chunk c8 of channel half ch is word 8 ch + c8 of a token row
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            uint32_t word = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) word |= code4x2(__half22float2(u2h2(x[k][j])), cmn[j], cs[j], crs[j]) << (8 * j);
-            codes[4 * k * WPR + 8 * ch + c8] = word;
-          }
+          for (int k = 0; k < 8; ++k) codes[4 * k * WPR + 8 * ch + c8] = codes4_chunk8(x[k], cmn, cs, crs);
         } else {
           uint32_t a1, a2, a3, b1, b2, b3;
           bool oa, ob;
@@ -323,7 +307,7 @@ __global__ void __launch_bounds__(kQThreads, kQCtas) packed_quantize_kernel(cons
           }
         }
       }
-      if (EXT || t0 + rows > nq) keep(ks, a.k.ts, a.k_res);
+      if (!EXT && t0 + rows > nq) keep(ks, a.k.ts, a.k_res);
     } else {
       const int q = lane & 3;
       uint4 y[2][4];
@@ -357,9 +341,15 @@ __global__ void __launch_bounds__(kQThreads, kQCtas) packed_quantize_kernel(cons
         const QParams p = make_qparams<BITS>(__low2float(red), -__high2float(red));
         uint32_t *codes_row = a.v_codes + (row0 + r) * WPR;
         if constexpr (BITS == 4) {
+          const float rs1 = p.s == 0.f ? 0.f : __frcp_rn(p.s);
+          const float2 m2 = make_float2(p.mn, p.mn), s2 = make_float2(p.s, p.s), r2 = make_float2(rs1, rs1);
+          const float2 mn[4] = {m2, m2, m2, m2}, s[4] = {s2, s2, s2, s2}, rs[4] = {r2, r2, r2, r2};
           if (ok_row) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) codes_row[q + 4 * k] = qchunk8<4>(y[i][k], p);
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t w[4] = {y[i][k].x, y[i][k].y, y[i][k].z, y[i][k].w};
+              codes_row[q + 4 * k] = codes4_chunk8(w, mn, s, rs);
+            }
           }
         } else {
           // lane q < 3 proves threshold q + 1 of the row (the second is the strict one)
@@ -395,20 +385,42 @@ __global__ void __launch_bounds__(kQThreads, kQCtas) packed_quantize_kernel(cons
         }
         if (ok_row && q == 0) a.v_meta[row0 + r] = p.meta;
       }
-      if (a.v_res && (EXT || t0 + rows > nq)) keep(vs, a.v.ts, a.v_res);
+      if (!EXT && a.v_res && t0 + rows > nq) keep(vs, a.v.ts, a.v_res);
     }
   }
 }
 
-// The sequences' new lengths, behind the quantizer.
-__global__ void __launch_bounds__(kPackedMaxSeqs) extend_lens_kernel(const PackedQuantArgs a) {
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const int s = threadIdx.x;
-  if (s >= a.B) return;
+// Behind the quantizer, a CTA a sequence: the new tokens that fill no group to the residual, and the new
+// length.  (Done in the quantizer itself, with a sequence's first unit, the CTAs that had those took
+// 10 us longer than the others.)
+constexpr int kTailThreads = 512;
+__global__ void __launch_bounds__(kTailThreads) extend_tail_kernel(const PackedQuantArgs a) {
+  const int s = blockIdx.x;
   const UnitWalk<true> u = {a.cu, a.B, a.T, a.max_pages << a.shift, 0, 0, 0, 0, a.seq_lens, 0};
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   int start, n, before;
   u.bounds(s, &start, &n, &before);
-  if (n > 0) a.seq_lens[s] = n;
+  if (n == 0) return;
+  const int nq = n / a.G * a.G, first = max(nq, before);
+  if (first < n) {
+    const int64_t page = a.bt[(int64_t)s * a.max_pages + (nq >> a.shift)];
+    if (page >= 0 && page < a.num_pages) {  // tokens without a page are dropped
+      const int rows = n - first, chunks = a.Hkv * rows * (kD / 8);
+      const int64_t at = (int64_t)start + first - before;  // row of position `first`
+#pragma unroll 4
+      for (int i = threadIdx.x; i < chunks; i += kTailThreads) {
+        const int c = i % (kD / 8), r = i / (kD / 8) % rows, h = i / (kD / 8) / rows;
+        const int64_t to = (((int64_t)s * a.Hkv + h) * a.G + first - nq + r) * kD + 8 * c;
+        *reinterpret_cast<uint4 *>(a.k_res + to) =
+            __ldg(reinterpret_cast<const uint4 *>(a.k.p + (at + r) * a.k.ts + h * a.k.hs) + c);
+        if (a.v_res)
+          *reinterpret_cast<uint4 *>(a.v_res + to) =
+              __ldg(reinterpret_cast<const uint4 *>(a.v.p + (at + r) * a.v.ts + h * a.v.hs) + c);
+      }
+    }
+  }
+  __syncthreads();  // every thread has read the length
+  if (threadIdx.x == 0) a.seq_lens[s] = n;
 }
 
 // One wave of CTAs, or fewer where there is less work.
@@ -417,7 +429,7 @@ cudaError_t launch_quantizer(const PackedQuantArgs &a, cudaStream_t st) {
   int sms = 0;
   const cudaError_t e = device_sms(&sms);
   if (e != cudaSuccess) return e;
-  const int64_t items = ((int64_t)a.T / kQUnit + (EXT ? 2 : 1) * a.B) * a.Hkv * 2, wave = (int64_t)sms * kQCtas;
+  const int64_t items = ((int64_t)a.T / kQUnit + (EXT ? 2 : 1) * a.B) * a.Hkv * 2, wave = (int64_t)sms * q_ctas(a.bits);
   const unsigned grid = (unsigned)(items < wave ? items : wave);
   if (a.bits == 2)
     packed_quantize_kernel<2, EXT><<<grid, kQThreads, 0, st>>>(a);
@@ -437,12 +449,12 @@ cudaError_t launch_packed_extend(const PackedQuantArgs &a, cudaStream_t st) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(kPackedMaxSeqs);
+  cfg.gridDim = dim3((unsigned)a.B);
+  cfg.blockDim = dim3(kTailThreads);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, extend_lens_kernel, a);
+  return cudaLaunchKernelEx(&cfg, extend_tail_kernel, a);
 }
 
 }  // namespace kivi

@@ -5,11 +5,15 @@
 // one rounding to fp16 (a half-precision fused multiply-add); beyond fp16's largest finite value it is that
 // value, so that the rows can be attended to.  Residual tokens are copied.
 //
-// What bounds it: 512 bytes written for every token and KV head, and 64 to 136 read.  The work is dealt
-// out in items of 32 positions of one KV head, keys and values, one warp each: a warp writes two whole
-// rows (512 bytes) at once, lane (t, c) chunk c of 8 channels of row t, so that the scales of a
-// key group's channels are read once an item and stay in registers.  Every warp takes a run of neighbouring
-// items (heads of the same positions first), so that the device's lengths are searched once a warp.
+// What bounds it: 512 bytes are written for every token and KV head, and 64 to 136 read, and this GPU writes
+// alone at 3.6 to 4.0 TB/s (cudaMemset's rate too; a copy moves 6.8, half of it reads).  32 sequences' 4099
+// tokens and 8 KV heads, 2-bit codes: 290 MB written in 68 us, 4.3 TB/s with what stays in L2.  The work is
+// dealt out in items of 32 positions of one KV head, keys and values, one warp each: a warp writes two
+// whole rows (512 bytes) at once, lane (t, c) chunk c of 8 channels of row t, so that the scales of a
+// key group's channels are read once an item and stay in registers.  The warps of a CTA take heads side by
+// side, so that the heads of a token, neighbours in memory, are written at about the same time (each warp a
+// run of its own: 80 us; four warps a CTA: 74).  More of an item's loads in flight, at fewer CTAs, were
+// slower (79 us).
 #include "kivi_device.cuh"
 #include "kivi_internal.h"
 #include "kivi_packed.cuh"
@@ -18,8 +22,8 @@ namespace kivi {
 
 namespace {
 
-constexpr int kBlock = 32, kThreads = 128, kWarps = kThreads / 32;
-constexpr int kCtas = 8;  // CTAs of an SM in one wave
+constexpr int kBlock = 32, kThreads = 256, kWarps = kThreads / 32;
+constexpr int kCtas = 4;  // CTAs of an SM in one wave (registers)
 
 // What is read of one sequence: positions 0 .. f - 1, then from .. n - 1, to rows row, row + 1, ..
 struct Piece {
@@ -41,23 +45,40 @@ __device__ __forceinline__ Piece piece_of(const ReadArgs &a, int b) {
   return p;
 }
 
-__device__ __forceinline__ uint32_t clamped(__half2 x) {
-  const __half2 top = u2h2(0x7bff7bffu);  // 65504
-  return h22u(__hmax2(__hmin2(x, top), __hneg2(top)));
-}
-
-// The 8 elements of a chunk from its codes (element i at bits BITS * i) and their {s, z}.
+// The 8 elements of a chunk from its codes (element i at bits BITS * i): z + code * s, of scale and zero
+// pairs s[j], z[j], at most the largest fp16 (the smallest is z: scales are not negative).
+// A code is masked into the mantissa of 1024, at bit 0, 4 or 8: 1024 + 16^i code, which one
+// multiply-add brings to the code, exactly.
 template <int BITS>
 __device__ __forceinline__ uint4 widen(uint32_t w, const __half2 s[4], const __half2 z[4]) {
-  const __half2 base = u2h2(0x64006400u);  // 1024: a code in its low bits adds to it
+  const uint32_t b = 0x64006400u;
+  const __half2 m1024 = u2h2(0xe400e400u), m64 = u2h2(0xd400d400u), m4 = u2h2(0xc400c400u);  // -1024 / 16^i
+  const __half2 i16 = u2h2(0x2c002c00u), i256 = u2h2(0x1c001c00u);                           // 1 / 16, 1 / 256
+  __half2 c[4];
+  if constexpr (BITS == 2) {
+    // codes 2 j (low half) and 2 j + 1 (high half) at bits 4 j; bits 14 and 15 of the low half are mixed up
+    const uint32_t y = w | (w << 14), y3 = y >> 8;
+    c[0] = __hadd2(u2h2((y & 0x00030003u) | b), m1024);
+    c[1] = __hfma2(u2h2((y & 0x00300030u) | b), i16, m64);
+    c[2] = __hfma2(u2h2((y & 0x03000300u) | b), i256, m4);
+    c[3] = __hfma2(u2h2((y3 & 0x00300030u) | b), i16, m64);
+  } else {
+    // codes j and j + 4, brought beside their neighbours below
+    const uint32_t y = w >> 8;
+    c[0] = __hadd2(u2h2((w & 0x000f000fu) | b), m1024);
+    c[1] = __hfma2(u2h2((w & 0x00f000f0u) | b), i16, m64);
+    c[2] = __hadd2(u2h2((y & 0x000f000fu) | b), m1024);
+    c[3] = __hfma2(u2h2((y & 0x00f000f0u) | b), i16, m64);
+    const uint32_t a = h22u(c[0]), d = h22u(c[1]), e = h22u(c[2]), f = h22u(c[3]);
+    c[0] = u2h2(prmt(a, d, 0x5410u));
+    c[1] = u2h2(prmt(e, f, 0x5410u));
+    c[2] = u2h2(prmt(a, d, 0x7632u));
+    c[3] = u2h2(prmt(e, f, 0x7632u));
+  }
   uint32_t o[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    // codes 2 j and 2 j + 1 to the low bits of the two halves
-    constexpr uint32_t kMask = (1u << BITS) - 1;
-    const uint32_t x = BITS * 2 * j ? w >> (BITS * 2 * j) : w;
-    const uint32_t c = (x & kMask) | ((x << (16 - BITS)) & (kMask << 16)) | 0x64006400u;
-    o[j] = clamped(__hfma2(__hsub2(u2h2(c), base), s[j], z[j]));
+    o[j] = h22u(__hmin2(__hfma2(c[j], s[j], z[j]), u2h2(0x7bff7bffu)));
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
@@ -80,9 +101,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_read_kernel(const ReadA
   // bounds that overlap can pass any count: cut at what lengths that do not overlap can reach
   const int64_t most = (int64_t)a.T / kBlock + 4 * a.B;
   const int64_t blocks = min(most, (int64_t)max(__shfl_sync(0xffffffffu, incl, 31), 0));
-  const int64_t items = blocks * a.Hkv, warps = (int64_t)gridDim.x * kWarps;
-  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int64_t first = items * w / warps, end = items * (w + 1) / warps;
+  const int64_t items = blocks * a.Hkv;
+  const int64_t first = items * blockIdx.x / gridDim.x + (threadIdx.x >> 5), end = items * (blockIdx.x + 1) / gridDim.x;
   if (first >= end) return;
   int64_t at = first / a.Hkv;
   int h = (int)(first - at * a.Hkv);
@@ -91,9 +111,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) paged_read_kernel(const ReadA
   int blk = (int)(at - __shfl_sync(0xffffffffu, incl - mine, owner));
   int b = min(owner * per, a.B - 1);
   Piece p = piece_of(a, b);
-  for (int64_t item = first; item < end; ++item, ++h) {
-    if (h == a.Hkv) {
-      h = 0;
+  for (int64_t item = first; item < end; item += kWarps, h += kWarps) {
+    while (h >= a.Hkv) {
+      h -= a.Hkv;
       ++blk;
     }
     while (blk >= p.blocks()) {
