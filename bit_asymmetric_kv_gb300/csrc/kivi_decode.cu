@@ -356,12 +356,13 @@ __device__ __forceinline__ int window_units(const DecodeArgs &a, int len, int *s
   return ncu - *skip;
 }
 
-template <int G>
+// COUNTED: U in counted units, else the units that are not empty.
+template <int G, bool COUNTED>
 __device__ __forceinline__ void set_window_geometry(const DecodeArgs &a, Cursor &c, int len) {
   c.NG = len / G;
   c.r = len - c.NG * G;
   c.ncu = window_units<G>(a, len, &c.su, &c.skip, &c.lo);
-  c.U = counted_units(c.ncu, c.r > 0);
+  c.U = COUNTED ? counted_units(c.ncu, c.r > 0) : c.ncu + (c.r > 0 ? 1 : 0);
 }
 
 template <int G>
@@ -625,8 +626,8 @@ __device__ __forceinline__ ResidualScores<R> residual_scores(const uint16_t *res
 // and no combine launch).  With CL > 1 the small path runs on a cluster of CL CTAs
 // per (batch, KV head), whose first CTA merges the partials of all of them.
 // kModeWindow is the persistent grid over a paged cache of which only a window of newest
-// tokens and the sinks are seen.
-constexpr int kModeDense = 0, kModePaged = 1, kModeSmall = 2, kModeWindow = 3;
+// tokens and the sinks are seen, kModeWindowSmall the small path over it.
+constexpr int kModeDense = 0, kModePaged = 1, kModeSmall = 2, kModeWindow = 3, kModeWindowSmall = 4;
 constexpr int kSmallWarps = kDecodeSmallWarps;
 
 // Partials of the small path: [warp][R] rows of kD + 2 floats after the warps' rings
@@ -636,9 +637,9 @@ __host__ __device__ constexpr int small_part_bytes() { return NW * R * (kD + 2) 
 
 template <int R, int G, int MODE, int BITS, int NWARPS, int VG = kD, int CL = 1>
 __device__ __forceinline__ void decode_body(const DecodeArgs &a) {
-  constexpr bool WIN = MODE == kModeWindow;
+  constexpr bool WIN = MODE == kModeWindow || MODE == kModeWindowSmall;
   constexpr bool PAGED = MODE == kModePaged || WIN;
-  constexpr bool SMALL = MODE == kModeSmall;
+  constexpr bool SMALL = MODE == kModeSmall || MODE == kModeWindowSmall;
   static_assert(CL == 1 || SMALL, "clusters: the small path only");
   extern __shared__ __align__(16) unsigned char smem[];
   using L = Layout<R, G, BITS, VG>;
@@ -668,7 +669,16 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a) {
   int2 *hdr = nullptr;
   float *part = a.ws;
   const int P = 1 << a.page_shift;
-  if constexpr (PAGED) {
+  Cursor own;  // paged small path: the CTA's head
+  if constexpr (PAGED && SMALL) {
+    own.h = blockIdx.x;
+    own.b = (int)(own.h / a.Hkv);
+    own.kvh = (int)(own.h - (int64_t)own.b * a.Hkv);
+    set_window_geometry<G, false>(a, own, min(max(a.seq_lens[own.b] + a.len_offset, 0), a.cap_tokens));
+    W = own.U;
+    NW = W < NWARPS ? W : NWARPS;
+    if (W == 0 && a.wait_tail) asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the lengths change behind this grid
+  } else if constexpr (PAGED) {
     s_len = reinterpret_cast<int *>(smem + L::kSmem);
     s_cum = s_len + a.B;
     paged_prefix<G, WIN>(a, s_len, s_cum);
@@ -694,7 +704,7 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a) {
     u0 = gw * W / NW;
     u1 = (gw + 1) * W / NW;
   }
-  if constexpr (SMALL) {
+  if constexpr (SMALL && !PAGED) {
     u0 += (int64_t)(blockIdx.x / CL) * W;
     u1 += (int64_t)(blockIdx.x / CL) * W;
   }
@@ -781,13 +791,16 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a) {
   Cursor ic;
   auto paged_geometry = [&](Cursor &c, int b) {
     if constexpr (WIN)
-      set_window_geometry<G>(a, c, s_len[b]);
+      set_window_geometry<G, true>(a, c, s_len[b]);
     else
       set_geometry<G>(c, s_len[b]);
   };
   // unit of the context that the cursor stands on (a unit of quantized keys)
   auto unit_of = [&](const Cursor &c) { return WIN && c.uu >= c.su ? c.uu + c.skip : c.uu; };
-  if constexpr (PAGED) {
+  if constexpr (PAGED && SMALL) {
+    ic = own;
+    ic.uu = (int)u0;
+  } else if constexpr (PAGED) {
     // the sequence holding unit u0: the last b with Hkv * cum[b] <= u0 (it has units)
     int lo = 0, hi = a.B - 1;
     while (lo < hi) {
@@ -808,7 +821,9 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a) {
   }
   Cursor cc = ic;
   auto advance = [&](Cursor &c) {
-    if (++c.uu == c.U) {
+    if constexpr (PAGED && SMALL) {
+      ++c.uu;
+    } else if (++c.uu == c.U) {
       c.uu = 0;
       if constexpr (PAGED) {
         if (++c.kvh == a.Hkv) {
@@ -1436,7 +1451,7 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a) {
   bool worked = false;  // with a window: this warp has had a unit of the head that is not empty
   for (int kk = 0; kk < n_my; ++kk) {
     issue(kk + AH);  // into the stage of unit kk - 1, which every lane has finished reading
-    if constexpr (PAGED) {
+    if constexpr (PAGED && !SMALL) {
       // the warp that takes a head's first unit publishes where its partials go
       if (cc.uu == 0 && lane == 0) {
         const int64_t start = (int64_t)a.Hkv * s_cum[cc.b] + (int64_t)cc.kvh * cc.U;
@@ -1528,6 +1543,19 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(NW * 32, 1) decode_
 template <int R, int G, int BITS>
 __global__ void __launch_bounds__(kThreads, KIVI_DECODE_MIN_CTAS) window_decode_kernel(const DecodeArgs a) {
   decode_body<R, G, kModeWindow, BITS, kWarps>(a);
+}
+
+// Windows that hold few units: one CTA per (sequence, KV head), its warps' partials merged in shared memory.
+template <int R, int G, int BITS>
+__global__ void __launch_bounds__(kSmallWarps * 32, 1) window_small_kernel(const DecodeArgs a) {
+  decode_body<R, G, kModeWindowSmall, BITS, kSmallWarps>(a);
+}
+
+// The lengths behind a step on the small path, as the combine kernel moves them.
+__global__ void __launch_bounds__(kPagedMaxBatch) window_advance_kernel(int32_t *seq_lens, int B, int32_t cap) {
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const int b = threadIdx.x;
+  if (b < B) seq_lens[b] = seq_lens[b] < cap ? seq_lens[b] + 1 : cap;
 }
 
 // Dense layout: the partials of (batch, query head) `row` sit at slots 0 .. np-1 of
@@ -1673,6 +1701,9 @@ DecodeKernels window_kernels_of(int extra) {
   k.smem = Layout<R, G, BITS>::kSmem + extra;
   k.smem_limit = Layout<R, G, BITS>::kSmem + paged_extra(kPagedMaxBatch);
   k.combine = reinterpret_cast<const void *>(&paged_combine_kernel);
+  k.small = reinterpret_cast<const void *>(&window_small_kernel<R, G, BITS>);
+  k.small_smem = kSmallWarps * Layout<R, G, BITS>::kWarpBytes + small_part_bytes<R>();
+  k.advance = reinterpret_cast<const void *>(&window_advance_kernel);
   return k;
 }
 

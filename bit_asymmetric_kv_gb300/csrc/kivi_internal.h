@@ -127,12 +127,13 @@ struct DecodeKernels {
   int smem_limit;
   const void *combine;  // dense: (ws, pmax, W, NW, U, Hkv, Hq, rows, out);
                         // paged: (ws, Hkv, Hq, B, advance, cap, out)
-  const void *small;    // dense only: one CTA of kDecodeSmallWarps warps per (batch, KV head)
+  const void *small;    // dense, and paged with a window: one CTA of kDecodeSmallWarps warps per (batch, KV head)
   int small_smem;
   const void *pair;     // dense only: a cluster of kDecodePairCtas CTAs per (batch, KV head)
   int pair_smem;
   const void *quad;     // dense only: a cluster of kDecodeQuadCtas CTAs per (batch, KV head)
   int quad_smem;
+  const void *advance;  // paged with a window: the lengths behind a step on the small path
 };
 // vg: channels per value scale (128, or 64 / 32 for value channel groups: dense
 // 2-bit caches only, no small-context kernel).

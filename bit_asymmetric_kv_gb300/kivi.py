@@ -463,7 +463,7 @@ def _run(call: str, device: torch.device, stream, *args) -> None:
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
     fn = getattr(_lib or lib(), call)
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == device.index:  # the tensors on it have initialised CUDA
         status = fn(*args, int(stream))
     else:
         with torch.cuda.device(device):
@@ -484,12 +484,12 @@ def _allocating_on(device: torch.device, stream):
 def _rows(t: torch.Tensor, name: str, device: torch.device) -> kivi_rows:
     """kivi_rows of an fp16 CUDA tensor [tokens, heads, D] with contiguous channels.  The stride of an
     axis of one element says nothing, and torch may hold any number there."""
-    shape, stride = t.shape, t.stride()
-    if t.dtype is not torch.float16 or not t.is_cuda or len(shape) != 3 or (stride[2] != 1 and t.numel()):
+    stride = t.stride()
+    if t.dtype is not torch.float16 or not t.is_cuda or len(stride) != 3 or (stride[2] != 1 and t.numel()):
         raise TypeError(f"{name}: expected a CUDA float16 tensor [tokens, heads, D] with contiguous channels")
-    if t.device != device:
+    if t.get_device() != device.index:
         raise ValueError(f"{name}: expected a tensor on {device}")
-    T, H, D = shape
+    T, H, D = t.shape
     return kivi_rows(t.data_ptr(), stride[0] if T > 1 else max(D, 128), stride[1] if H > 1 else max(D, 128))
 
 
@@ -497,7 +497,7 @@ def _i32(t: torch.Tensor, name: str, numel: int, device: torch.device) -> int:
     """Address of a contiguous int32 tensor of `numel` elements on `device`."""
     if t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous() or t.numel() != numel:
         raise TypeError(f"{name}: expected a contiguous CUDA int32 tensor of {numel} elements")
-    if t.device != device:
+    if t.get_device() != device.index:
         raise ValueError(f"{name}: expected a tensor on {device}")
     return t.data_ptr()
 
@@ -574,12 +574,12 @@ def kivi_prefill_attention_window(q: torch.Tensor, k: torch.Tensor, v: torch.Ten
 
 def _heads(t: torch.Tensor, name: str, cache: PagedCache, heads: int | None = None) -> torch.Tensor:
     """An fp16 tensor [B, heads, D] of one token a sequence, contiguous and on the cache's device."""
-    d = cache.dims
+    d, shape = cache.dims, t.shape
     _f16(t, name)
-    if t.device != cache.k_codes.device:
+    if t.get_device() != cache.k_codes.get_device():
         raise ValueError(f"{name}: expected a tensor on {cache.k_codes.device}")
-    if t.dim() != 3 or t.shape[0] != d.B or t.shape[2] != d.D or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name}: {list(t.shape)}, expected [{d.B}, {heads or 'heads'}, {d.D}]")
+    if len(shape) != 3 or shape[0] != d.B or shape[2] != d.D or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name}: {list(shape)}, expected [{d.B}, {heads or 'heads'}, {d.D}]")
     return t
 
 
@@ -592,10 +592,10 @@ def _decode_window(call: str, cache: PagedCache, new: list, q: torch.Tensor, win
             out = torch.empty_like(q) if out is None else out
             ws = paged_workspace(cache, Hq, device=dev) if ws is None else ws
     _heads(out, "out", cache, Hq)
-    if not ws.is_cuda or ws.device != dev or not ws.is_contiguous():
+    if ws.get_device() != dev.index or not ws.is_contiguous():
         raise ValueError(f"ws: expected a contiguous tensor on {dev}")
-    _run(call, dev, stream, cache.dims, cache.c, *[t.data_ptr() for t in new], q.data_ptr(), Hq, float(softmax_scale),
-         window, sinks, out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+    _run(call, dev, stream, cache.dims, cache.c, *new, q.data_ptr(), Hq, float(softmax_scale), window, sinks,
+         out.data_ptr(), ws.data_ptr(), ws.nbytes)
     return out
 
 
@@ -613,7 +613,7 @@ def kivi_paged_decode_step_window(cache: PagedCache, k_new: torch.Tensor, v_new:
                                   ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """kivi_paged_decode_step in which the appended token sees the newest `window` tokens, itself among them,
     and the first `sinks`."""
-    new = [_heads(k_new, "k_new", cache, cache.dims.Hkv), _heads(v_new, "v_new", cache, cache.dims.Hkv)]
+    new = [_heads(t, name, cache, cache.dims.Hkv).data_ptr() for t, name in ((k_new, "k_new"), (v_new, "v_new"))]
     return _decode_window("kivi_paged_decode_step_window", cache, new, q, window, sinks, softmax_scale, out, ws, stream)
 
 
