@@ -538,7 +538,9 @@ template <int R>
 struct ResidualScores {
   float s[R][2];
 };
-template <int R, int G>
+// DEEP: all chunks' loads of a pair of keys may be in flight, where the registers allow it (the small path,
+// on which a warp's own latency is what counts).
+template <int R, int G, bool DEEP>
 __device__ __forceinline__ ResidualScores<R> residual_scores(const uint16_t *res_head, const uint16_t *q_row, int r) {
   const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
   ResidualScores<R> out;
@@ -559,7 +561,7 @@ __device__ __forceinline__ ResidualScores<R> residual_scores(const uint16_t *res
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int hh = 0; hh < R; ++hh) s2[i][hh] = make_float2(0.f, 0.f);
-#pragma unroll 1
+#pragma unroll DEEP ? 4 : 1
       for (int c = 0; c < 4; ++c) {
         uint4 kx[2];
 #pragma unroll
@@ -1332,7 +1334,7 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a) {
     // layout becomes (score, 0).
     float sc[R][4];
     if constexpr (WIN) {
-      const ResidualScores<R> s = residual_scores<R, G>(res_head, cursor_q(cc), r);
+      const ResidualScores<R> s = residual_scores<R, G, SMALL>(res_head, cursor_q(cc), r);
 #pragma unroll
       for (int rho = 0; rho < R; ++rho) {
         sc[rho][0] = s.s[rho][0];
