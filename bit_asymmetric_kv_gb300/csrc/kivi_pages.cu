@@ -206,6 +206,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
   __shared__ Shared sh;
   __shared__ int s_rank[64];  // missing entries of this CTA's rows, then the rank of each row's first
   __shared__ int s_freed;     // WIN, of the first CTA: pages given back
+  __shared__ int2 s_span[64];  // WIN: first and last of a row's missing entries
   cg::cluster_group cl = cg::this_cluster();
   if (WIN && threadIdx.x == 0) s_freed = 0;
   cl.barrier_arrive();  // this CTA runs: see exchange()
@@ -225,19 +226,35 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
     int32_t *row = a.bt + (int64_t)(b0 + i) * a.max_pages;
     int c = 0;
     if constexpr (WIN) {
-      int from = 0, to = 0;
+      int from = 0, to = 0;  // to <= m: an unseen entry's positions lie below the length
       if (m > 0) unseen_entries(a, a.seq_lens[b0 + i], &from, &to);
-#pragma unroll 4
-      for (int j = lane; j < m; j += 32) c += !in_pool(a, row[j]) && !(j >= from && j < to);
-      int freed = 0;
-      for (int j = from + lane; j < to; j += 32) {
-        const int page = row[j];
-        if (page == -1) continue;
-        row[j] = -1;
-        if (in_pool(a, page)) freed += atomicAdd(a.refs + page, -1) == 1;
+      int freed = 0, lowest = m, highest = -1;
+      for (int j0 = lane; j0 < m; j0 += 256) {  // eight loads in flight
+        int page[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) page[u] = j0 + 32 * u < m ? row[j0 + 32 * u] : 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int j = j0 + 32 * u;
+          if (j >= m) break;
+          const bool held = in_pool(a, page[u]);
+          if (j >= from && j < to) {
+            if (page[u] != -1) row[j] = -1;
+            if (held) freed += atomicAdd(a.refs + page[u], -1) == 1;
+          } else if (!held) {
+            ++c;
+            lowest = min(lowest, j);
+            highest = max(highest, j);
+          }
+        }
       }
       freed = __reduce_add_sync(0xffffffffu, freed);
-      if (lane == 0 && freed) gone += freed;
+      lowest = __reduce_min_sync(0xffffffffu, lowest);
+      highest = __reduce_max_sync(0xffffffffu, highest);
+      if (lane == 0) {
+        gone += freed;
+        s_span[i] = make_int2(lowest, highest);
+      }
     } else {
 #pragma unroll 4
       for (int j = lane; j < m; j += 32) c += !in_pool(a, row[j]);
@@ -270,12 +287,16 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
     const int m = entries(b0 + i);
     int32_t *row = a.bt + (int64_t)(b0 + i) * a.max_pages;
     int k = s_rank[i];
-    int from = 0, to = 0;
-    if (WIN && m > 0) unseen_entries(a, a.seq_lens[b0 + i], &from, &to);
-    for (int j0 = 0; j0 < m; j0 += 128) {  // four loads in flight
+    int from = 0, to = 0, begin = 0, end = m;
+    if constexpr (WIN) {
+      if (m > 0) unseen_entries(a, a.seq_lens[b0 + i], &from, &to);
+      begin = s_span[i].x;
+      end = s_span[i].y + 1;
+    }
+    for (int j0 = begin; j0 < end; j0 += 128) {  // four loads in flight
       int page[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) page[u] = j0 + 32 * u + lane < m ? row[j0 + 32 * u + lane] : 0;
+      for (int u = 0; u < 4; ++u) page[u] = j0 + 32 * u + lane < end ? row[j0 + 32 * u + lane] : 0;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int j = j0 + 32 * u + lane;
