@@ -3,6 +3,8 @@ launch.  No test here touches device memory."""
 from __future__ import annotations
 
 import math
+import os
+import re
 
 import pytest
 import torch
@@ -133,3 +135,12 @@ def test_binding_refuses(L):
             kivi._count(bad, "window", 1)
     with pytest.raises(ValueError):
         kivi._count(-1, "sinks", 0)
+
+
+@pytest.mark.parametrize("source", ["kivi_window_attention.cu", "kivi_read.cu"])
+def test_grids_follow_the_device(source):
+    """As test_launch_grids.py for the sources of these calls."""
+    with open(os.path.join(kbuild.CSRC, source)) as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    assert not re.search(r"\b(132|144|148|152|160)\b", code)  # SMs of a device as a number
+    assert "device_sms(" in code
