@@ -561,7 +561,7 @@ __device__ __forceinline__ ResidualScores<R> residual_scores(const uint16_t *res
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int hh = 0; hh < R; ++hh) s2[i][hh] = make_float2(0.f, 0.f);
-#pragma unroll DEEP ? 4 : 1
+#pragma unroll DEEP ? 4 : 2
       for (int c = 0; c < 4; ++c) {
         uint4 kx[2];
 #pragma unroll
@@ -860,6 +860,7 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a) {
   int64_t pg_next = 0;  // page of ic's unit, loaded one unit ahead of its use
   if constexpr (PAGED) {
     if (ic.uu < ic.ncu) pg_next = page_of(ic.b, unit_of(ic) * kUnit);
+    else if (WIN && ic.on_residual()) pg_next = page_of(ic.b, ic.NG * G);
   }
 
   bool waited = false;
@@ -905,10 +906,25 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a) {
       const unsigned char *res = reinterpret_cast<const unsigned char *>(a.k_res + ic.h * G * kD);
       for (int i = 128 * lane; i < ic.r * kD * 2; i += 128 * 32)
         asm volatile("prefetch.global.L2 [%0];\n" ::"l"(res + i));
+      if (!a.v_res) {  // its values are staged as a unit's are, in whole 16 bytes of scales
+        const int rows = (ic.r + 3) & ~3, nq = ic.NG * G;
+        const int64_t row0 = (pg_next * a.Hkv + ic.kvh) * P + (nq & (P - 1));
+        const int st = kk % S;
+        if (lane == 0) {
+          const uint32_t bar = bar0 + 8 * st;
+          const uint32_t dst = smem_addr(wbase + st * L::kStageBytes);
+          asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+          mbar_arm(bar, (uint32_t)rows * (L::kRowBytes + 4));
+          bulk_copy(dst + L::kVCodes, a.v_codes + row0 * WPR, (uint32_t)rows * L::kRowBytes, bar);
+          bulk_copy(dst + L::kVMeta, a.v_meta + row0, (uint32_t)rows * 4, bar);
+        }
+        armed |= 1u << st;
+      }
     }
     advance(ic);
     if constexpr (PAGED) {
       if (kk + 1 < n_my && ic.uu < ic.ncu) pg_next = page_of(ic.b, unit_of(ic) * kUnit);
+      else if (WIN && kk + 1 < n_my && ic.on_residual()) pg_next = page_of(ic.b, ic.NG * G);
     }
   };
 
@@ -1316,12 +1332,13 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a) {
 
   // ---- the residual unit of a head: its r fp16 keys (read from the residual buffer)
   // and their values (quantized rows nq .. nq + r - 1, or the fp16 value residual)
-  auto residual_unit = [&]() {
+  auto residual_unit = [&](const unsigned char *stg) {
     const int r = cc.r;
     const int64_t nq = (int64_t)cc.NG * G;
     const uint16_t *res_head = a.k_res + cc.h * G * kD;
-    int64_t vrow;  // value row of token nq (one page: pages hold whole groups)
-    if constexpr (PAGED) {
+    int64_t vrow = 0;  // value row of token nq (one page: pages hold whole groups); staged with a window
+    if constexpr (WIN) {
+    } else if constexpr (PAGED) {
       const int64_t ph = page_of(cc.b, (int)nq) * a.Hkv + cc.kvh;
       vrow = ph * P + (nq & (P - 1));
     } else {
@@ -1378,7 +1395,13 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a) {
     const uint32_t *vm_head = a.v_meta + vrow * NV;
     uint32_t bw0[R], bw1[R];
     float pp[R][2];
-    auto vmeta = [&](int tok, int m) -> uint32_t { return a.v_res ? 0x00003C00u : __ldg(vm_head + tok * NV + m); };
+    auto vmeta = [&](int tok, int m) -> uint32_t {
+      if (a.v_res) return 0x00003C00u;
+      if constexpr (WIN)
+        return lds32(stg + L::kVMeta + tok * 4);
+      else
+        return __ldg(vm_head + tok * NV + m);
+    };
     const float alpha = update(
         std::false_type{}, sc, [&](int) { return c0; }, [&](int) { return 0.f; }, r, vmeta, bw0, bw1, pp);
     if constexpr (NV > 1) {
@@ -1421,7 +1444,17 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a) {
           if (16 * t < r) {
             const bool mine = pv_slot == i;
             const uint32_t b0 = mine ? bw0[rho] : 0u, b1 = mine ? bw1[rho] : 0u;
-            if constexpr (BITS == 2) {
+            if constexpr (WIN && BITS == 2) {  // rows behind the r meet weight 0
+              uint32_t v[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) v[k] = lds32(stg + L::kVCodes + (16 * t + tig + 4 * k) * 32 + g * 4);
+              pv_tile(acc, v, b0, b1);
+            } else if constexpr (WIN) {
+              uint2 v[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) v[k] = lds64(stg + L::kVCodes + (16 * t + tig + 4 * k) * 64 + g * 8);
+              pv_tile4(acc, v, b0, b1);
+            } else if constexpr (BITS == 2) {
               uint32_t v[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
@@ -1488,11 +1521,20 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a) {
           code_unit(std::false_type{}, stg, ngr * G);
       }
     } else if (!WIN || cc.on_residual()) {
+      const int st = kk % S;
       if constexpr (WIN) {
         win_lo = cc.lo - cc.NG * G;
         win_sinks = a.sinks - cc.NG * G;
+        if (!a.v_res) {
+          if (!mbar_wait(bar0 + 8 * st, (phase >> st) & 1u)) {
+            fault = true;
+            break;
+          }
+          phase ^= 1u << st;
+          armed &= ~(1u << st);
+        }
       }
-      residual_unit();
+      residual_unit(wbase + st * L::kStageBytes);
     }
     __syncwarp();  // this unit's stage and the fragment may be rewritten from now on
     if constexpr (WIN) worked |= cc.uu <= cc.last();
