@@ -391,11 +391,12 @@ __global__ void __launch_bounds__(kQThreads, q_ctas(BITS)) packed_quantize_kerne
 }
 
 // Behind the quantizer, a CTA a sequence: the new tokens that fill no group to the residual, and the new
-// length.  (Done in the quantizer itself, with a sequence's first unit, the CTAs that had those took
-// 10 us longer than the others.)
-constexpr int kTailThreads = 512;
+// length.  Thread (r, c) takes chunk c of row r (there are at most 63) of every head, eight heads in
+// flight.  (Done in the quantizer itself, with a sequence's first unit, the CTAs that had those took 10 us
+// longer than the others.)
+constexpr int kTailThreads = 64 * (kD / 8);
 __global__ void __launch_bounds__(kTailThreads) extend_tail_kernel(const PackedQuantArgs a) {
-  const int s = blockIdx.x;
+  const int s = blockIdx.x, r = threadIdx.x / (kD / 8), c = threadIdx.x % (kD / 8);
   const UnitWalk<true> u = {a.cu, a.B, a.T, a.max_pages << a.shift, 0, 0, 0, 0, a.seq_lens, 0};
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   int start, n, before;
@@ -404,19 +405,23 @@ __global__ void __launch_bounds__(kTailThreads) extend_tail_kernel(const PackedQ
   const int nq = n / a.G * a.G, first = max(nq, before);
   if (first < n) {
     const int64_t page = a.bt[(int64_t)s * a.max_pages + (nq >> a.shift)];
-    if (page >= 0 && page < a.num_pages) {  // tokens without a page are dropped
-      const int rows = n - first, chunks = a.Hkv * rows * (kD / 8);
-      const int64_t at = (int64_t)start + first - before;  // row of position `first`
-#pragma unroll 4
-      for (int i = threadIdx.x; i < chunks; i += kTailThreads) {
-        const int c = i % (kD / 8), r = i / (kD / 8) % rows, h = i / (kD / 8) / rows;
-        const int64_t to = (((int64_t)s * a.Hkv + h) * a.G + first - nq + r) * kD + 8 * c;
-        *reinterpret_cast<uint4 *>(a.k_res + to) =
-            __ldg(reinterpret_cast<const uint4 *>(a.k.p + (at + r) * a.k.ts + h * a.k.hs) + c);
-        if (a.v_res)
-          *reinterpret_cast<uint4 *>(a.v_res + to) =
-              __ldg(reinterpret_cast<const uint4 *>(a.v.p + (at + r) * a.v.ts + h * a.v.hs) + c);
-      }
+    if (page >= 0 && page < a.num_pages && first + r < n) {  // tokens without a page are dropped
+      const int64_t row = (int64_t)start + first - before + r;
+      auto copy = [&](const PackedRows &from, uint16_t *res) {
+        const uint16_t *src = from.p + row * from.ts + 8 * c;
+        uint16_t *dst = res + ((int64_t)s * a.Hkv * a.G + first - nq + r) * kD + 8 * c;
+        for (int h0 = 0; h0 < a.Hkv; h0 += 8) {
+          uint4 x[8];
+#pragma unroll
+          for (int h = 0; h < 8; ++h)
+            if (h0 + h < a.Hkv) x[h] = __ldg(reinterpret_cast<const uint4 *>(src + (h0 + h) * from.hs));
+#pragma unroll
+          for (int h = 0; h < 8; ++h)
+            if (h0 + h < a.Hkv) *reinterpret_cast<uint4 *>(dst + (int64_t)(h0 + h) * a.G * kD) = x[h];
+        }
+      };
+      copy(a.k, a.k_res);
+      if (a.v_res) copy(a.v, a.v_res);
     }
   }
   __syncthreads();  // every thread has read the length
