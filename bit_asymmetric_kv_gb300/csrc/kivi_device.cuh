@@ -255,13 +255,14 @@ __device__ __forceinline__ uint32_t code4x2(float2 x, float2 mn, float2 s, float
 
 // Eight 4-bit codes at once, x[j] the fp16 pair of elements 2j, 2j + 1; code i at bits 4i.  The same
 // values as code4x2's: d = fl(x - mn), q = fl(d * rs) and r = rint(q) decide unless an element lies
-// within 2^-15 of a half-integer (or its rint is beyond 15: subnormal scales), and then
-// an exact comparison stands for the division: next to m = h + 1/2, m * s is exact (6 and 11 bits), and
-// fl(d / s) > m exactly when d > m * s, since d is then at least one ulp of m * s above it, which
-// is more than s * ulp(m) / 2; fl(d / s) < m exactly when d < m * s, likewise.  One check for all
-// eight: a branch for each of them took most of the quantizer's time.
-__device__ __forceinline__ uint32_t codes4_chunk8(const uint32_t (&x)[4], const float2 (&mn)[4], const float2 (&s)[4],
-                                                  const float2 (&rs)[4]) {
+// within 2^-15 of a half-integer, or its rint is beyond 15 (subnormal scales): `unsure`, one check for
+// all eight, after which codes4_exact says what they are.
+__device__ __forceinline__ uint32_t join4x8(const float (&v)[4]) {  // v[j] = code 2j + 16 code 2j + 1
+  const float lo = fmaf(v[1], 256.f, v[0]) + 8388608.f, hi = fmaf(v[3], 256.f, v[2]) + 8388608.f;
+  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410);
+}
+__device__ __forceinline__ uint32_t codes4_chunk8(const uint32_t (&x)[4], const float2 (&mn)[4], const float2 (&rs)[4],
+                                                  bool &unsure) {
   constexpr float kM = 12582912.f;  // 1.5 * 2^23
   float v[4], far = 0.f, top = 0.f;
 #pragma unroll
@@ -274,21 +275,27 @@ __device__ __forceinline__ uint32_t codes4_chunk8(const uint32_t (&x)[4], const 
     top = fmaxf(top, fmaxf(q.x, q.y));
     v[j] = fmaf(r.y, 16.f, r.x);  // integers below 2^24 all along: exact
   }
-  if (far > 0.5f - 0x1p-15f || top > 15.25f) {
+  unsure = far > 0.5f - 0x1p-15f || top > 15.25f;
+  return join4x8(v);
+}
+// The same codes with an exact comparison in the division's place: next to m = h + 1/2, m * s is exact
+// (6 and 11 bits), and fl(d / s) > m exactly when d > m * s, since d is then at least one ulp of m * s
+// above it, which is more than s * ulp(m) / 2; fl(d / s) < m exactly when d < m * s, likewise.
+__device__ __forceinline__ uint32_t codes4_exact(const uint32_t (&x)[4], const float2 (&mn)[4], const float2 (&s)[4],
+                                                 const float2 (&rs)[4]) {
+  float v[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 d = __fadd2_rn(__half22float2(u2h2(x[j])), make_float2(-mn[j].x, -mn[j].y));
-      const float2 q = __fmul2_rn(d, rs[j]);
-      auto code = [](float d, float q, float s) {
-        const float h = floorf(q), m = h + 0.5f, ms = __fmul_rn(m, s);
-        const float near = d > ms ? h + 1.f : (d < ms ? h : rintf(m));
-        return fminf(fabsf(q - m) < 0x1p-14f ? near : rintf(q), 15.f);
-      };
-      v[j] = fmaf(code(d.y, q.y, s[j].y), 16.f, code(d.x, q.x, s[j].x));
-    }
+  for (int j = 0; j < 4; ++j) {
+    const float2 d = __fadd2_rn(__half22float2(u2h2(x[j])), make_float2(-mn[j].x, -mn[j].y));
+    const float2 q = __fmul2_rn(d, rs[j]);
+    auto code = [](float d, float q, float s) {
+      const float h = floorf(q), m = h + 0.5f, ms = __fmul_rn(m, s);
+      const float near = d > ms ? h + 1.f : (d < ms ? h : rintf(m));
+      return fminf(fabsf(q - m) < 0x1p-14f ? near : rintf(q), 15.f);
+    };
+    v[j] = fmaf(code(d.y, q.y, s[j].y), 16.f, code(d.x, q.x, s[j].x));
   }
-  const float lo = fmaf(v[1], 256.f, v[0]) + 8388608.f, hi = fmaf(v[3], 256.f, v[2]) + 8388608.f;
-  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410);
+  return join4x8(v);
 }
 
 // One code of either width; rs = 1/s (used by 4-bit codes only).

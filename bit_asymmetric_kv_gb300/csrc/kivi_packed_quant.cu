@@ -255,8 +255,21 @@ __global__ void __launch_bounds__(kQThreads, q_ctas(BITS)) packed_quantize_kerne
             crs[j] = make_float2(__shfl_sync(0xffffffffu, rs0, sl), __shfl_sync(0xffffffffu, rs1, sl));
           }
           // chunk c8 of channel half ch is word 8 ch + c8 of a token row
+          uint32_t unsure = 0;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) codes[4 * k * WPR + 8 * ch + c8] = codes4_chunk8(x[k], cmn, cs, crs);
+          for (int k = 0; k < 8; ++k) {
+            bool bad;
+            codes[4 * k * WPR + 8 * ch + c8] = codes4_chunk8(x[k], cmn, crs, bad);
+            unsure |= (uint32_t)bad << k;
+          }
+          // rows that need the exact comparison (one in 60 of a warp's): read again, so that this is one loop
+#pragma unroll 1
+          for (; unsure; unsure &= unsure - 1) {
+            const int k = __ffs(unsure) - 1;
+            const uint4 y = chunk(ks, a.k.ts, a.k_res, 32 * rh + t4 + 4 * k, 8 * ch + c8);
+            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+            codes[4 * k * WPR + 8 * ch + c8] = codes4_exact(w, cmn, cs, crs);
+          }
         } else {
           uint32_t a1, a2, a3, b1, b2, b3;
           bool oa, ob;
@@ -345,10 +358,20 @@ __global__ void __launch_bounds__(kQThreads, q_ctas(BITS)) packed_quantize_kerne
           const float2 m2 = make_float2(p.mn, p.mn), s2 = make_float2(p.s, p.s), r2 = make_float2(rs1, rs1);
           const float2 mn[4] = {m2, m2, m2, m2}, s[4] = {s2, s2, s2, s2}, rs[4] = {r2, r2, r2, r2};
           if (ok_row) {
+            uint32_t unsure = 0;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t w[4] = {y[i][k].x, y[i][k].y, y[i][k].z, y[i][k].w};
-              codes_row[q + 4 * k] = codes4_chunk8(w, mn, s, rs);
+              bool bad;
+              codes_row[q + 4 * k] = codes4_chunk8(w, mn, rs, bad);
+              unsure |= (uint32_t)bad << k;
+            }
+#pragma unroll 1
+            for (; unsure; unsure &= unsure - 1) {
+              const int k = __ffs(unsure) - 1;
+              const uint4 z = chunk(vs, a.v.ts, a.v_res, r, q + 4 * k);
+              const uint32_t w[4] = {z.x, z.y, z.z, z.w};
+              codes_row[q + 4 * k] = codes4_exact(w, mn, s, rs);
             }
           }
         } else {
