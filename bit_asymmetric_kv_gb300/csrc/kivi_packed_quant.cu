@@ -13,7 +13,14 @@
 // memory), and derives the parameters of channel pair t4 of its chunk.  Values: a row is
 // held by 4 lanes.
 //
-// Measured on 16 prompts of up to 8192 tokens, 8 KV heads, G = 64: 43 us, 0.55 of the measured
+// Chunks behind what the sequences hold (kivi_paged_extend_packed) are the same units, those of 64 positions
+// that hold a new token, with the rows before in the residual.
+//
+// Measured on 32 prompts of 500 to 2048 tokens, 8 KV heads, 4 bits, G = 64: 54 us, appended as chunks 64 us (0.41 of the
+// measured copy bandwidth; 2 bits: 48 and 59 us), the kernel for the tails and a launch among them.
+// 4-bit codes one by one, each with a branch to a division, took 91 us, eight with one check and the exact form
+// inline 64: `no instruction` was and is the first stall.
+// Measured on 16 prompts of up to 8192 tokens, 8 KV heads, G = 64, 2 bits: 43 us, 0.55 of the measured
 // copy bandwidth.  No unit is full: the integer and comparison unit is busy for 53% of the
 // cycles, as is the scheduler; waits for a unit's loads, which go out when the unit before is
 // stored, and for code that every warp reads anew take the rest.  Units found one by one by a CTA each took 58 us, keys held as
@@ -32,7 +39,7 @@ constexpr int kQUnit = 64, kQThreads = 128;
 
 static_assert(kPackedMaxSeqs == kPagedMaxBatch, "a packed batch is a paged batch");
 // CTAs that fit on an SM (registers): a launch is one wave of them.  4-bit codes hold the parameters of
-// a chunk's channels beside its rows (32 prompts of up to 2048 tokens: 64 us at five, 66 at six, 70 at seven).
+// a chunk's channels beside its rows (32 prompts of up to 2048 tokens: 54 us at five, 56 at six and seven).
 constexpr int q_ctas(int bits) { return bits == 2 ? 7 : 5; }
 
 // Where a run of units stands.  EXT: the new tokens stand behind what the sequences hold; the units
