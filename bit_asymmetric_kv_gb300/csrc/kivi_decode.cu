@@ -332,15 +332,18 @@ struct Cursor {
   __device__ __forceinline__ int last() const { return r > 0 ? ncu : ncu - 1; }
 };
 
-// With a window a head's work is counted in units of what a unit of codes takes: the residual
-// unit counts as two, of which the first holds it and the other is empty, and each head
-// has two more, empty, for its query, its partials and their merge.  A warp's share of a batch of
-// short and long contexts is then worth the same (64 sequences of 100 to 32808 tokens, window
-// 4096, four heads: 56 us; 60 with one for the head, 90 with the residual as one and none for the
-// head).
-constexpr int kResidualUnits = 2, kHeadUnits = 2;
-__device__ __forceinline__ int counted_units(int code_units, bool residual) {
-  return code_units + (residual ? kResidualUnits : 0) + (code_units || residual ? kHeadUnits : 0);
+// With a window a head's work is counted in units of what a unit of codes takes a warp, so that the
+// warps' shares of a batch of short and long contexts are worth the same: the residual unit counts as
+// several, of which the first holds it and the others are empty, and each head has some more, empty, for
+// its query, its partials and their merge.  Measured on batches of equal sequences: a residual unit takes 5 units'
+// time with four heads and 3 with one, a head 4.6 and 2.6.  (64 sequences of 100 to 32808 tokens, window
+// 4096, four heads: 52 us at 4 and 4, 56 at 2 and 2, 90 at 1 and 0.)  Where the units are no more than the
+// warps, each has a warp of its own and nothing is counted.
+template <int R>
+__device__ __forceinline__ int counted_units(int code_units, bool residual, bool counted) {
+  constexpr int kResidual = R == 1 ? 3 : 4, kHead = R == 1 ? 2 : R == 2 ? 3 : 4;
+  if (!counted) return code_units + (residual ? 1 : 0);
+  return code_units + (residual ? kResidual : 0) + (code_units || residual ? kHead : 0);
 }
 
 // Units of a context of `len` tokens that hold a token that its last one sees: the sinks'
@@ -356,13 +359,12 @@ __device__ __forceinline__ int window_units(const DecodeArgs &a, int len, int *s
   return ncu - *skip;
 }
 
-// COUNTED: U in counted units, else the units that are not empty.
-template <int G, bool COUNTED>
-__device__ __forceinline__ void set_window_geometry(const DecodeArgs &a, Cursor &c, int len) {
+template <int R, int G>
+__device__ __forceinline__ void set_window_geometry(const DecodeArgs &a, Cursor &c, int len, bool counted) {
   c.NG = len / G;
   c.r = len - c.NG * G;
   c.ncu = window_units<G>(a, len, &c.su, &c.skip, &c.lo);
-  c.U = COUNTED ? counted_units(c.ncu, c.r > 0) : c.ncu + (c.r > 0 ? 1 : 0);
+  c.U = counted_units<R>(c.ncu, c.r > 0, counted);
 }
 
 template <int G>
@@ -377,38 +379,63 @@ __device__ __forceinline__ void set_geometry(Cursor &c, int64_t len) {
 // Paged layout: per-sequence lengths (clamped to the block table's capacity) and the
 // exclusive prefix sum of the sequences' unit counts, in shared memory.  All threads
 // of the CTA take part; B <= 4 * kThreads.
-template <int G, bool WIN>
-__device__ void paged_prefix(const DecodeArgs &a, int *s_len, int *s_cum) {
+// WIN: in counted units where there are more units than warps, which is returned; both are summed side by side.
+template <int R, int G, bool WIN>
+__device__ bool paged_prefix(const DecodeArgs &a, int *s_len, int *s_cum) {
   constexpr int NGU = kUnit / G;
-  int *s_tot = s_cum + a.B + 1;
+  int *s_tot = s_cum + a.B + 1;  // of every warp (WIN: and in counted units)
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  int u[4], loc = 0;
+  int u[4], v[4], loc = 0, loc2 = 0;  // v, loc2: counted units
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int b = 4 * t + j;
-    u[j] = 0;
+    u[j] = v[j] = 0;
     if (b < a.B) {
       int len = a.seq_lens[b] + a.len_offset;
       len = len < 0 ? 0 : (len > a.cap_tokens ? a.cap_tokens : len);
       s_len[b] = len;
       const int ng = len / G;
+      const bool rest = len - ng * G > 0;
       if constexpr (WIN) {
         int su, skip, lo;
-        u[j] = counted_units(window_units<G>(a, len, &su, &skip, &lo), len - ng * G > 0);
+        const int codes = window_units<G>(a, len, &su, &skip, &lo);
+        u[j] = counted_units<R>(codes, rest, false);
+        v[j] = counted_units<R>(codes, rest, true);
       } else {
-        u[j] = (ng + NGU - 1) / NGU + (len - ng * G > 0 ? 1 : 0);
+        u[j] = (ng + NGU - 1) / NGU + (rest ? 1 : 0);
       }
     }
     loc += u[j];
+    loc2 += v[j];
   }
-  int inc = loc;
+  int inc = loc, inc2 = loc2;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const int y = __shfl_up_sync(kFull, inc, off);
     if (lane >= off) inc += y;
+    if constexpr (WIN) {
+      const int y2 = __shfl_up_sync(kFull, inc2, off);
+      if (lane >= off) inc2 += y2;
+    }
   }
-  if (lane == 31) s_tot[warp] = inc;
+  if (lane == 31) {
+    s_tot[warp] = inc;
+    if constexpr (WIN) s_tot[kWarps + warp] = inc2;
+  }
   __syncthreads();
+  bool counted = false;
+  if constexpr (WIN) {
+    int64_t units = 0;
+    for (int w = 0; w < kWarps; ++w) units += s_tot[w];
+    counted = units * a.Hkv > a.n_warps;
+    if (counted) {
+      loc = loc2;
+      inc = inc2;
+      s_tot += kWarps;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] = v[j];
+    }
+  }
   int ex = inc - loc;
   for (int w = 0; w < warp; ++w) ex += s_tot[w];
 #pragma unroll
@@ -419,6 +446,7 @@ __device__ void paged_prefix(const DecodeArgs &a, int *s_len, int *s_cum) {
   }
   if (t == kThreads - 1) s_cum[a.B] = ex;  // the total
   __syncthreads();
+  return counted;
 }
 
 // Merge np partials (max, sum, unnormalised output; `stride` floats apart) of one
@@ -672,18 +700,19 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a) {
   float *part = a.ws;
   const int P = 1 << a.page_shift;
   Cursor own;  // paged small path: the CTA's head
+  bool counted = false;
   if constexpr (PAGED && SMALL) {
     own.h = blockIdx.x;
     own.b = (int)(own.h / a.Hkv);
     own.kvh = (int)(own.h - (int64_t)own.b * a.Hkv);
-    set_window_geometry<G, false>(a, own, min(max(a.seq_lens[own.b] + a.len_offset, 0), a.cap_tokens));
+    set_window_geometry<R, G>(a, own, min(max(a.seq_lens[own.b] + a.len_offset, 0), a.cap_tokens), false);
     W = own.U;
     NW = W < NWARPS ? W : NWARPS;
     if (W == 0 && a.wait_tail) asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the lengths change behind this grid
   } else if constexpr (PAGED) {
     s_len = reinterpret_cast<int *>(smem + L::kSmem);
     s_cum = s_len + a.B;
-    paged_prefix<G, WIN>(a, s_len, s_cum);
+    counted = paged_prefix<R, G, WIN>(a, s_len, s_cum);
     W = (int64_t)a.Hkv * s_cum[a.B];
     hdr = reinterpret_cast<int2 *>(a.ws);
     part = a.ws + 2 * (int64_t)a.B * a.Hkv;
@@ -793,7 +822,7 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a) {
   Cursor ic;
   auto paged_geometry = [&](Cursor &c, int b) {
     if constexpr (WIN)
-      set_window_geometry<G, true>(a, c, s_len[b]);
+      set_window_geometry<R, G>(a, c, s_len[b], counted);
     else
       set_geometry<G>(c, s_len[b]);
   };
@@ -1740,15 +1769,16 @@ int smem_bytes(int R, int G) {
   return R == 1 ? Layout<1, 64, BITS>::kSmem : R == 2 ? Layout<2, 64, BITS>::kSmem : Layout<4, 64, BITS>::kSmem;
 }
 
-// Paged kernels append the lengths, the unit prefix and 4 warp totals: 2B + 5 ints.
-constexpr int paged_extra(int B) { return (4 * (2 * B + 5) + 15) & ~15; }
+// Paged kernels append the lengths, the unit prefix and 4 warp totals: 2B + 5 ints (with a window,
+// 4 more totals).
+constexpr int paged_extra(int B, int more = 0) { return (4 * (2 * B + 5 + more) + 15) & ~15; }
 
 template <int R, int G, int BITS>
 DecodeKernels window_kernels_of(int extra) {
   DecodeKernels k = {};
   k.decode = reinterpret_cast<const void *>(&window_decode_kernel<R, G, BITS>);
   k.smem = Layout<R, G, BITS>::kSmem + extra;
-  k.smem_limit = Layout<R, G, BITS>::kSmem + paged_extra(kPagedMaxBatch);
+  k.smem_limit = Layout<R, G, BITS>::kSmem + paged_extra(kPagedMaxBatch, kWarps);
   k.combine = reinterpret_cast<const void *>(&paged_combine_kernel);
   k.small = reinterpret_cast<const void *>(&window_small_kernel<R, G, BITS>);
   k.small_smem = kSmallWarps * Layout<R, G, BITS>::kWarpBytes + small_part_bytes<R>();
@@ -1798,7 +1828,7 @@ DecodeKernels decode_kernels(int R, int G, int bits, bool paged, int B, int vg) 
 }
 
 DecodeKernels decode_window_kernels(int R, int G, int bits, int B) {
-  const int extra = paged_extra(B);
+  const int extra = paged_extra(B, kWarps);
   return R == 1 ? window_of_shape<1>(G, bits, extra) : R == 2 ? window_of_shape<2>(G, bits, extra) : window_of_shape<4>(G, bits, extra);
 }
 

@@ -171,6 +171,25 @@ def test_lengths_that_make_no_sense_are_clamped():
     close(out, reference(c, q, 50, 2))
 
 
+@pytest.mark.parametrize("window,sinks", [(70, 4), (2000, 4)])  # one CTA a head, and the whole grid
+@pytest.mark.parametrize("v_res", [False, True])
+def test_steps_at_the_capacity(window, sinks, v_res):
+    """A full sequence drops the token and attends to what it holds."""
+    lens = [640, 640 - 1, 200, 0, 31]
+    a = filled(lens, 2, 32, 64, 2, v_res, seed=14)
+    b = filled(lens, 2, 32, 64, 2, v_res, seed=14)
+    for c in (a, b):
+        assert c.dims.max_pages_per_seq == 10
+        c.block_table[3, 0] = c.dims.num_pages - 1
+    for step in range(3):
+        k, v = (torch.randn((5, 2, D), device="cuda", generator=torch.Generator("cuda").manual_seed(step)).to(torch.float16) for _ in "kv")
+        q = aimed(a, 8, window, sinks, step)
+        out = kivi.kivi_paged_decode_step_window(a, k, v, q, window, sinks, SCALE)
+        kivi.kivi_paged_append_token(b, k, v)
+        assert a.seq_lens.tolist() == b.seq_lens.tolist() == [640, 640, 201 + step, 1 + step, 32 + step]
+        close(out, reference(b, q, window, sinks))
+
+
 def test_offsets_past_32_bits():
     """Pages whose code words lie past element 2^31."""
     Hkv, P, lens = 8, 64, [300, 70]
