@@ -1613,7 +1613,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(NW * 32, 1) decode_
 // dealt out in the same units, of which only those that hold a visible token count.  Pages that hold no
 // such unit are neither looked up nor read, so their table entries may hold anything.  Masks cost only
 // in the unit at each end.
-// Measured: 64 sequences of 100 to 32808 tokens, window 4096 and 4 sinks, 32 query heads on 8, 2 bits: 49 us, 1.5 TB/s
+// Measured: 64 sequences of 100 to 32808 tokens, window 4096 and 4 sinks, 32 query heads on 8, 2 bits: 48 us, 1.6 TB/s
 // of what is visible; 64 of 4096 tokens each: 71 us, 2.2 TB/s, as over whole contexts (65 us).  Bound by
 // instructions and their latency: 12 warps an SM, a scheduler busy for 44% of the cycles, the integer unit for
 // 39%.  A unit's codes take a warp 2.9 us; a residual unit takes 5 times that with four heads (3 with one), a head's
