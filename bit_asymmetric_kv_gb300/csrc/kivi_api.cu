@@ -594,7 +594,10 @@ int kivi_paged_append_token(const kivi_paged_dims *d, const kivi_paged_cache *c,
 
 size_t kivi_paged_decode_workspace_bytes(const kivi_paged_dims *d, int32_t Hq) {
   if (check_paged_dims(d) != KIVI_OK || check_paged_heads(d, Hq) != KIVI_OK) return 0;
+  // The windows' geometry is asked for too: behind this query no paged decode call of these sizes asks the
+  // runtime, so that all of them can be captured.
   kivi::PagedGeom g;
+  if (kivi::paged_decode_geometry(d->B, d->Hkv, Hq, d->G, d->bits, &g, true) != cudaSuccess) return 0;
   if (kivi::paged_decode_geometry(d->B, d->Hkv, Hq, d->G, d->bits, &g) != cudaSuccess) return 0;
   return g.ws_bytes;
 }

@@ -3,7 +3,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <map>
 #include <mutex>
+#include <tuple>
 
 #include "kivi_internal.h"
 
@@ -20,18 +22,22 @@ constexpr int kD = 128;
 // the occupancy calculator; later calls read a table, so that decode calls make no
 // CUDA runtime query but cudaGetDevice (and can be captured in a CUDA graph once a
 // first call has run).
+// The paged kernels' size grows with the batch (256 values up to B = 512), so the table has
+// no fixed number of entries: a process that serves every batch size keeps them all.
 struct WarpsEntry {
-  int dev;
-  const void *fn;
-  int smem;
   int n_warps;
   int sms;
   int pair_clusters;  // clusters of the pair kernel resident at once (0 without one)
   int quad_clusters;  // the same for the quad kernel
 };
-constexpr int kWarpsCache = 256;
-WarpsEntry g_warps[kWarpsCache];
-int g_warps_used = 0;
+using WarpsKey = std::tuple<int, const void *, int>;  // device, kernel, shared memory
+// never destroyed: a call may come from another static's destructor
+union WarpsTable {
+  std::map<WarpsKey, WarpsEntry> map;
+  WarpsTable() : map() {}
+  ~WarpsTable() {}
+};
+WarpsTable g_warps;
 std::mutex g_warps_lock;
 
 // Clusters of `fn` (CTAs of `warps` warps with `smem` bytes; its cluster shape is fixed
@@ -51,16 +57,17 @@ cudaError_t warps_on_device(const DecodeKernels &k, int *n_warps, int *n_sms = n
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const WarpsKey key(dev, k.decode, k.smem);
   {
     std::lock_guard<std::mutex> guard(g_warps_lock);
-    for (int i = 0; i < g_warps_used; ++i)
-      if (g_warps[i].dev == dev && g_warps[i].fn == k.decode && g_warps[i].smem == k.smem) {
-        *n_warps = g_warps[i].n_warps;
-        if (n_sms) *n_sms = g_warps[i].sms;
-        if (n_pairs) *n_pairs = g_warps[i].pair_clusters;
-        if (n_quads) *n_quads = g_warps[i].quad_clusters;
-        return cudaSuccess;
-      }
+    const auto it = g_warps.map.find(key);
+    if (it != g_warps.map.end()) {
+      *n_warps = it->second.n_warps;
+      if (n_sms) *n_sms = it->second.sms;
+      if (n_pairs) *n_pairs = it->second.pair_clusters;
+      if (n_quads) *n_quads = it->second.quad_clusters;
+      return cudaSuccess;
+    }
   }
   e = cudaFuncSetAttribute(k.decode, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem_limit);
   if (e != cudaSuccess) return e;
@@ -83,9 +90,11 @@ cudaError_t warps_on_device(const DecodeKernels &k, int *n_warps, int *n_sms = n
   if (n_sms) *n_sms = sms;
   if (n_pairs) *n_pairs = pairs;
   if (n_quads) *n_quads = quads;
-  std::lock_guard<std::mutex> guard(g_warps_lock);
-  if (g_warps_used < kWarpsCache)
-    g_warps[g_warps_used++] = WarpsEntry{dev, k.decode, k.smem, *n_warps, sms, pairs, quads};
+  try {
+    std::lock_guard<std::mutex> guard(g_warps_lock);
+    g_warps.map[key] = WarpsEntry{*n_warps, sms, pairs, quads};
+  } catch (...) {  // no host memory for an entry: asked again next time
+  }
   return cudaSuccess;
 }
 
@@ -155,11 +164,11 @@ cudaError_t paged_decode_geometry(int B, int Hkv, int Hq, int G, int bits, Paged
   int nw = 0;
   cudaError_t e = warps_on_device(decode_kernels(R, G, bits, true, B), &nw);
   if (e != cudaSuccess) return e;
-  // the window's kernel is asked about here too, so that any call or query before a graph's
-  // capture has both kernels' answers on record
-  int win = 0;
-  if ((e = warps_on_device(decode_window_kernels(R, G, bits, B), &win)) != cudaSuccess) return e;
-  if (window && win < nw) nw = win;
+  if (window) {
+    int win = 0;
+    if ((e = warps_on_device(decode_window_kernels(R, G, bits, B), &win)) != cudaSuccess) return e;
+    if (win < nw) nw = win;
+  }
   const size_t heads = (size_t)B * Hkv;
   out->n_warps = nw;
   out->grid = nw / kDecodeWarps;

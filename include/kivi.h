@@ -64,10 +64,11 @@
  * for the small-context path's thread-block clusters) and records the
  * answer in a table inside the library, guarded by a mutex; later calls only read
  * it, so they make no runtime query but cudaGetDevice and can be captured in a CUDA
- * graph.  Make a first decode call (or a kivi_decode_workspace_bytes /
- * kivi_paged_decode_workspace_bytes query) on each device before capturing.  The
- * table holds no cache data and never changes a result.  The allocation-free entry
- * point keeps a second table (see kivi_decode_attention_noalloc).
+ * graph.  Make a first call of the same kind and sizes, or a kivi_decode_workspace_bytes /
+ * kivi_paged_decode_workspace_bytes query for them (the latter asks for calls with and
+ * without a window), on each device before capturing.  The table holds no cache data
+ * and never changes a result.  The allocation-free entry point keeps a second table
+ * (see kivi_decode_attention_noalloc).
  *
  * Device dependence: the split of the context between the GPU's warps, and with it
  * kivi_decode_splits, kivi_decode_workspace_bytes and
