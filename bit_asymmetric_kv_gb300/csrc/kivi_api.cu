@@ -608,6 +608,9 @@ static int paged_decode(const kivi_paged_dims *d, const kivi_paged_cache *c, boo
                         int32_t sinks, uint16_t *out, void *ws, size_t ws_bytes, cudaStream_t st) {
   int s = check_paged_dims(d);
   if (s != KIVI_OK) return s;
+  // a window's units are counted with more than the whole context's, for which check_paged_dims answers
+  if (window > 0 && (int64_t)d->B * (paged_cap(d) / kivi::kDecodeUnit + kivi::kWindowExtraUnits) > INT32_MAX)
+    return KIVI_ERR_UNSUPPORTED;
   if ((s = check_paged_cache(d, c)) != KIVI_OK) return s;
   if ((s = check_paged_heads(d, Hq)) != KIVI_OK) return s;
   if ((step && (!k_new || !v_new)) || !q || !out) return KIVI_ERR_ARG;

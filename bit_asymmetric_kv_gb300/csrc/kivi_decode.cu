@@ -342,6 +342,7 @@ struct Cursor {
 template <int R>
 __device__ __forceinline__ int counted_units(int code_units, bool residual, bool counted) {
   constexpr int kResidual = R == 1 ? 3 : 4, kHead = R == 1 ? 2 : R == 2 ? 3 : 4;
+  static_assert(kResidual + kHead <= kWindowExtraUnits, "the host's bound on counted units");
   if (!counted) return code_units + (residual ? 1 : 0);
   return code_units + (residual ? kResidual : 0) + (code_units || residual ? kHead : 0);
 }

@@ -163,6 +163,9 @@ struct PagedGeom {
   size_t ws_bytes;
 };
 constexpr int kPagedMaxBatch = 512;
+// With a window, what a sequence's units are counted as at most, beyond its units of codes: the residual and
+// the head's own work.  Their sums are int32 on the device.
+constexpr int kWindowExtraUnits = 8;
 // `window`: of the kernel over a window.  It never has more warps than the other: one workspace
 // serves both.
 cudaError_t paged_decode_geometry(int B, int Hkv, int Hq, int G, int bits, PagedGeom *out, bool window = false);

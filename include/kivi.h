@@ -387,7 +387,8 @@ KIVI_API int kivi_paged_decode_step(const kivi_paged_dims *dims, const kivi_page
  * one likes.  Only the pages that hold a visible token are looked up and read: a page that lies outside the window
  * and behind the sinks may be given to another sequence, and its table entry hold anything
  * (kivi_paged_reserve_window does that on the device).  A key group counts as read when a token of it is
- * visible.  Workspace: kivi_paged_decode_workspace_bytes().
+ * visible.  B * (max_pages_per_seq * P / 64 + 8) at most 2^31 - 1 (KIVI_ERR_UNSUPPORTED).  Workspace:
+ * kivi_paged_decode_workspace_bytes().
  */
 KIVI_API int kivi_paged_decode_attention_window(const kivi_paged_dims *dims, const kivi_paged_cache *cache,
                                                 const uint16_t *q, int32_t Hq, float softmax_scale, int32_t window,
