@@ -573,16 +573,16 @@ template <int R, int G, bool DEEP>
 __device__ __forceinline__ ResidualScores<R> residual_scores(const uint16_t *res_head, const uint16_t *q_row, int r) {
   const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
   ResidualScores<R> out;
-      const uint4 *kp = reinterpret_cast<const uint4 *>(res_head) + tig;
-      const uint4 *qp = reinterpret_cast<const uint4 *>(q_row) + tig;
-      const bool b0 = tig & 1, b1 = tig & 2;
-      float one[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // R = 1: of each half, tile b0 of it
-  #pragma unroll
-      for (int rho = 0; rho < R; ++rho) out.s[rho][0] = out.s[rho][1] = 0.f;
-  #pragma unroll
-      for (int half = 0; half < G / 32; ++half) {
-        if (32 * half >= r) break;
-        float s1[4][R];
+  const uint4 *kp = reinterpret_cast<const uint4 *>(res_head) + tig;
+  const uint4 *qp = reinterpret_cast<const uint4 *>(q_row) + tig;
+  const bool b0 = tig & 1, b1 = tig & 2;
+  float one[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // R = 1: of each half, tile b0 of it
+#pragma unroll
+  for (int rho = 0; rho < R; ++rho) out.s[rho][0] = out.s[rho][1] = 0.f;
+#pragma unroll
+  for (int half = 0; half < G / 32; ++half) {
+    if (32 * half >= r) break;
+    float s1[4][R];
 #pragma unroll
     for (int two = 0; two < 4; two += 2) {
       float2 s2[2][R];
@@ -624,30 +624,30 @@ __device__ __forceinline__ ResidualScores<R> residual_scores(const uint16_t *res
         for (int hh = 0; hh < R; ++hh) s1[two + i][hh] = s2[i][hh].x + s2[i][hh].y;
     }
     // keys 2 u and 2 u + 1 of the four are tokens g and g + 8 of tile 2 half + u
-        auto fold = [&](float lo, float hi, bool up, int off) {  // the sum over the pair of lanes, of `hi` in the upper one
-          return (up ? hi : lo) + __shfl_xor_sync(kFull, up ? lo : hi, off);
-        };
-  #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if constexpr (R == 4) {
-  #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const float x = fold(s1[2 * u + j][0], s1[2 * u + j][1], b0, 1), y = fold(s1[2 * u + j][2], s1[2 * u + j][3], b0, 1);
-              out.s[2 * half + u][j] = fold(x, y, b1, 2);
-            }
-          } else if constexpr (R == 2) {
-            const float x = fold(s1[j][0], s1[j][1], b0, 1), y = fold(s1[2 + j][0], s1[2 + j][1], b0, 1);
-            out.s[half][j] = fold(x, y, b1, 2);
-          } else {
-            one[half][j] = fold(s1[j][0], s1[2 + j][0], b0, 1);
-          }
+    auto fold = [&](float lo, float hi, bool up, int off) {  // the sum over the pair of lanes, of `hi` in the upper one
+      return (up ? hi : lo) + __shfl_xor_sync(kFull, up ? lo : hi, off);
+    };
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if constexpr (R == 4) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float x = fold(s1[2 * u + j][0], s1[2 * u + j][1], b0, 1), y = fold(s1[2 * u + j][2], s1[2 * u + j][3], b0, 1);
+          out.s[2 * half + u][j] = fold(x, y, b1, 2);
         }
+      } else if constexpr (R == 2) {
+        const float x = fold(s1[j][0], s1[j][1], b0, 1), y = fold(s1[2 + j][0], s1[2 + j][1], b0, 1);
+        out.s[half][j] = fold(x, y, b1, 2);
+      } else {
+        one[half][j] = fold(s1[j][0], s1[2 + j][0], b0, 1);
       }
-      if constexpr (R == 1) {
-  #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          out.s[0][j] = (b1 ? one[1][j] : one[0][j]) + __shfl_xor_sync(kFull, b1 ? one[0][j] : one[1][j], 2);
-      }
+    }
+  }
+  if constexpr (R == 1) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      out.s[0][j] = (b1 ? one[1][j] : one[0][j]) + __shfl_xor_sync(kFull, b1 ? one[0][j] : one[1][j], 2);
+  }
   return out;
 }
 
@@ -1391,34 +1391,34 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a) {
     } else {
       const uint4 *qp = reinterpret_cast<const uint4 *>(cursor_q(cc) + head_mine * kD);
 #pragma unroll
-    for (int rho = 0; rho < R; ++rho) {
-      const int sa = 16 * (rho * T + slot_mine) + g, sb = sa + 8;
-      const bool va = sa < r, vb = sb < r;
-      const uint4 *ka = reinterpret_cast<const uint4 *>(res_head + (va ? sa : 0) * kD);
-      const uint4 *kb = reinterpret_cast<const uint4 *>(res_head + (vb ? sb : 0) * kD);
-      float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
-      if (va || vb) {  // the two keys of the lane share each query load
+      for (int rho = 0; rho < R; ++rho) {
+        const int sa = 16 * (rho * T + slot_mine) + g, sb = sa + 8;
+        const bool va = sa < r, vb = sb < r;
+        const uint4 *ka = reinterpret_cast<const uint4 *>(res_head + (va ? sa : 0) * kD);
+        const uint4 *kb = reinterpret_cast<const uint4 *>(res_head + (vb ? sb : 0) * kD);
+        float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
+        if (va || vb) {  // the two keys of the lane share each query load
 #pragma unroll 4
-        for (int c = 0; c < kD / 8; ++c) {
-          const uint4 qq = __ldg(qp + c), xa = __ldg(ka + c), xb = __ldg(kb + c);
-          const uint32_t qw[4] = {qq.x, qq.y, qq.z, qq.w}, wa[4] = {xa.x, xa.y, xa.z, xa.w};
-          const uint32_t wb[4] = {xb.x, xb.y, xb.z, xb.w};
+          for (int c = 0; c < kD / 8; ++c) {
+            const uint4 qq = __ldg(qp + c), xa = __ldg(ka + c), xb = __ldg(kb + c);
+            const uint32_t qw[4] = {qq.x, qq.y, qq.z, qq.w}, wa[4] = {xa.x, xa.y, xa.z, xa.w};
+            const uint32_t wb[4] = {xb.x, xb.y, xb.z, xb.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 fq = __half22float2(u2h2(qw[i]));
-            const float2 fa2 = __half22float2(u2h2(wa[i])), fb2 = __half22float2(u2h2(wb[i]));
-            a0 = fmaf(fq.x, fa2.x, a0);
-            a1 = fmaf(fq.y, fa2.y, a1);
-            b0 = fmaf(fq.x, fb2.x, b0);
-            b1 = fmaf(fq.y, fb2.y, b1);
+            for (int i = 0; i < 4; ++i) {
+              const float2 fq = __half22float2(u2h2(qw[i]));
+              const float2 fa2 = __half22float2(u2h2(wa[i])), fb2 = __half22float2(u2h2(wb[i]));
+              a0 = fmaf(fq.x, fa2.x, a0);
+              a1 = fmaf(fq.y, fa2.y, a1);
+              b0 = fmaf(fq.x, fb2.x, b0);
+              b1 = fmaf(fq.y, fb2.y, b1);
+            }
           }
         }
+        sc[rho][0] = va ? a0 + a1 : 0.f;
+        sc[rho][1] = 0.f;
+        sc[rho][2] = vb ? b0 + b1 : 0.f;
+        sc[rho][3] = 0.f;
       }
-      sc[rho][0] = va ? a0 + a1 : 0.f;
-      sc[rho][1] = 0.f;
-      sc[rho][2] = vb ? b0 + b1 : 0.f;
-      sc[rho][3] = 0.f;
-    }
     }
     // residual values are quantized ({s, z} of their row) or, with a value residual,
     // fp16 themselves: weight p with s = 1, z = 0
@@ -1674,6 +1674,7 @@ __global__ void __launch_bounds__(32 * kCombineRows) paged_combine_kernel(const 
     advance[b] = len < cap ? len + 1 : cap;
   }
 }
+
 template <int R, int G, bool PAGED, int BITS>
 const void *kernel_ptr() {
   return reinterpret_cast<const void *>(&decode_kernel<R, G, PAGED, BITS>);
