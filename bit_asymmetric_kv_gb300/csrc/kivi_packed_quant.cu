@@ -19,7 +19,8 @@
 // Measured on 32 prompts of 500 to 2048 tokens, 8 KV heads, 4 bits, G = 64: 54 us, appended as chunks 64 us (0.41 of the
 // measured copy bandwidth; 2 bits: 48 and 59 us), the kernel for the tails and a launch among them.
 // 4-bit codes one by one, each with a branch to a division, took 91 us, eight with one check and the exact form
-// inline 64: `no instruction` was and is the first stall.
+// inline 64, with `no instruction` the first stall (2.4 an issue).  With the exact form in a loop of its own that is 0.3; a warp
+// waits for a unit's loads (1.7 an issue) and for its own results (1.4), and a scheduler issues in 58% of the cycles.
 // Measured on 16 prompts of up to 8192 tokens, 8 KV heads, G = 64, 2 bits: 43 us, 0.55 of the measured
 // copy bandwidth.  No unit is full: the integer and comparison unit is busy for 53% of the
 // cycles, as is the scheduler; waits for a unit's loads, which go out when the unit before is

@@ -25,8 +25,8 @@
 // Roles, tensor memory, the softmax's arithmetic and its rounding are those of the attention over
 // whole prompts (kivi_packed_attention.cu).
 //
-// Measured: two prompts of 16384 and 8200 tokens, window 4096, 32 query heads on 8: 1.06 ms, 1.30 PFLOP/s of
-// visible work, 0.67 of the measured bf16 peak (tensor pipe 56%); 16 chunks of 200 to 512 tokens behind up to 4099
+// Measured: two prompts of 16384 and 8200 tokens, window 4096, 32 query heads on 8: 1.12 ms a call, 1.07 of
+// them the kernel, 1.29 PFLOP/s of visible work in it, 0.66 of the measured bf16 peak (tensor pipe 56%); 16 chunks of 200 to 512 tokens behind up to 4099
 // earlier ones, the same heads: 0.17 ms, 0.44; eight ragged prompts of up to 4113 tokens, window 1024 and 4 sinks, 32
 // heads: 0.37 ms, 0.42.  What bounds it: a tile's pass is a chain (scores, softmax, P.V) of about 3300
 // cycles, of which its own MMAs are 1024, and the two tiles overlap only in part, as over whole prompts.  A
