@@ -1615,8 +1615,9 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(NW * 32, 1) decode_
 // such unit are neither looked up nor read, so their table entries may hold anything.  Masks cost only
 // in the unit at each end.
 // Measured: 64 sequences of 100 to 32808 tokens, window 4096 and 4 sinks, 32 query heads on 8, 2 bits: 48 us, 1.6 TB/s
-// of what is visible; 64 of 4096 tokens each, behind a flush of L2: 70 us against the whole-context kernel's 64, since counted heads leave a warp without a change of head up to 20 units where an even deal gives 18.
-// Four heads spill 42 to 78 bytes here; window_small_kernel<4, 64, *> 650 to 990 (its `DEEP` scoring).  Bound by
+// of what is visible; 64 of 4096 tokens each, behind a flush of L2: 70 us against the whole-context kernel's 64,
+// since counted heads leave a warp without a change of head up to 20 units where an even deal gives 18.  Four
+// heads spill 42 to 78 bytes here; window_small_kernel<4, 64, *> 650 to 990 (its `DEEP` scoring).  Bound by
 // instructions and their latency: 12 warps an SM, a scheduler busy for 44% of the cycles, the integer unit for
 // 39%.  A unit's codes take a warp 2.9 us; a residual unit takes 5 times that with four heads (3 with one), a head's
 // query, partials and merge 4.6 (2.6), which is why the ragged batch is the slower one for what it reads.

@@ -25,17 +25,19 @@
 // Roles, tensor memory, the softmax's arithmetic and its rounding are those of the attention over
 // whole prompts (kivi_packed_attention.cu).
 //
-// Measured: two prompts of 16384 and 8200 tokens, window 4096, 32 query heads on 8: 1.12 ms a call, 1.07 of
-// them the kernel, 1.29 PFLOP/s of visible work in it, 0.66 of the measured bf16 peak (tensor pipe 56%); 16 chunks of 200 to 512 tokens behind up to 4099
-// earlier ones, the same heads: 0.17 ms, 0.44; eight ragged prompts of up to 4113 tokens, window 1024 and 4 sinks, 32
-// heads: 0.37 ms, 0.42.  What bounds it: a tile's pass is a chain (scores, softmax, P.V) of about 3300
-// cycles, of which its own MMAs are 1024, and the two tiles overlap only in part, as over whole prompts.  A
-// window of w tiles costs a tile w + 1 passes, half of the first and of the last masked, and one more for the
-// sinks: 10 where 8 would hold the visible keys, in the third case.  Tried and not faster there: a sinks' pass of 32
-// columns (a second form of the softmax costs every pass 2%, as much as it saves), the passes of all blocks as one
-// stream (the next block's first scores beside a block's last product: level; with the choices made at each product,
-// 11% slower).  Sorting blocks by the level in their own sequence, as the attention over whole prompts does, made
-// the chunks behind earlier tokens 1.25 times slower.
+// Measured: two prompts of 16384 and 8200 tokens, window 4096, 32 query heads on 8: 1.12 ms a call,
+// 1.07 of them the kernel, 1.29 PFLOP/s of visible work in it, 0.66 of the measured bf16 peak
+// (tensor pipe 56%); 16 chunks of 200 to 512 tokens behind up to 4099 earlier ones, the same heads:
+// 0.17 ms, 0.44; eight ragged prompts of up to 4113 tokens, window 1024 and 4 sinks, 32 heads: 0.37
+// ms, 0.42.  What bounds it: a tile's pass is a chain (scores, softmax, P.V) of about 3300 cycles,
+// of which its own MMAs are 1024, and the two tiles overlap only in part, as over whole prompts.  A
+// window of w tiles costs a tile w + 1 passes, half of the first and of the last masked, and one
+// more for the sinks: 10 where 8 would hold the visible keys, in the third case.  Tried and not
+// faster there: a sinks' pass of 32 columns (a second form of the softmax costs every pass 2%, as
+// much as it saves), the passes of all blocks as one stream (the next block's first scores beside a
+// block's last product: level; with the choices made at each product, 11% slower).  Sorting blocks
+// by the level in their own sequence, as the attention over whole prompts does, made the chunks
+// behind earlier tokens 1.25 times slower.
 //
 // Every wait is bounded: one that runs out (a copy that never completes) ends all roles
 // of the CTA; the rows of its block are NaN, those of its later blocks not written.

@@ -501,8 +501,9 @@ KIVI_API int kivi_paged_extend_packed(const kivi_paged_dims *dims, const kivi_pa
  * in order; its row i is position i for i < first, else position n - c + i.  With take[s] = its rows less those of
  * the next chunk, the chunk's own keys and values have their place behind them.  Rows behind the c are left as
  * they were.  An element is fp16(z + code * s) of the exact product and sum, rounded once, at most 65504 in
- * magnitude.  What the residual holds is copied, whatever the table says (keys, and values with a value residual);
- * anything else of a position whose table entry lies outside the pool reads as zeros.  Elements of k_out and v_out must not overlap one another (KIVI_ERR_ARG within each).
+ * magnitude.  What the residual holds is copied, whatever the table says (keys, and values with a value
+ * residual); anything else of a position whose table entry lies outside the pool reads as zeros.  Elements of
+ * k_out and v_out must not overlap one another (KIVI_ERR_ARG within each).
  */
 KIVI_API int kivi_paged_read(const kivi_paged_dims *dims, const kivi_paged_cache *cache, const int32_t *cu_seqlens,
                              int64_t n_tokens, const int32_t *take, int32_t first, const kivi_rows *k_out,
